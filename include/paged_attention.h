@@ -75,6 +75,9 @@ typedef enum pa_dtype {
                                      was ignored; those sequences were attended in full, so
                                      the output is still exact                            */
 
+#define PA_ERRBIT_AXIS        128 /* pa_rope_append: a pair_axis entry outside [0, num_axes):
+                                     that pair is not turned (angle 0)                      */
+
 /* Human-readable name of a status code (static storage). */
 const char *pa_status_str(pa_status status);
 
@@ -197,6 +200,63 @@ pa_status pa_reshape_and_cache(const void *key, const void *value, void *k_cache
                                void *v_cache, const int64_t *slot_mapping, int num_tokens,
                                int num_kv_heads, int head_dim, int block_size, int num_blocks,
                                pa_dtype dtype, int32_t *err_flag, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Slot write with rotary positions (rope_append)
+ * ------------------------------------------------------------------------
+ * pa_reshape_and_cache for models that turn their queries and keys by the
+ * token's position, with the rotation on the way: the step's q rows go
+ * rotated to q_out (ready for pa_decode, pa_prefill, ...), its key rows
+ * rotated to their slots, its value rows unchanged to theirs.  Pair i of the
+ * first rotary_dim dims of a row, i < rotary_dim / 2, is
+ *     (a, b) = (x[i], x[i + rotary_dim / 2])      PA_ROPE_HALVES
+ *              (x[2 i], x[2 i + 1])               PA_ROPE_ADJACENT
+ * and becomes
+ *     theta = positions[axis][t] * inv_freq[i],   axis = pair_axis[i]
+ *     (a, b) <- rot_scale * (a cos theta - b sin theta, a sin theta + b cos theta)
+ * Dims from rotary_dim on are copied bit for bit.  theta is reduced in 64
+ * bits, so far positions cost no accuracy (positions are taken as exact up
+ * to 2^53); the products are fp32 and each result is rounded once
+ * (nearest-even) to the element type.
+ *
+ *   q, q_out       [num_tokens] rows of num_q_heads * head_dim elements, row
+ *                  t at t * q_stride (q_out_stride) elements.  q_out may be q
+ *                  itself, with the same stride.  Both NULL: only append.
+ *   key, value     [num_tokens] rows of num_kv_heads * head_dim elements, at
+ *                  t * key_stride and t * value_stride.  The strides let all
+ *                  three be views of one fused projection.
+ *   k_cache, v_cache, slot_mapping (int64 [num_tokens])  as in
+ *                  pa_reshape_and_cache: a negative slot is padding (its q
+ *                  row is rotated all the same), slots must be distinct, one
+ *                  past the cache sets PA_ERRBIT_SLOT and writes nothing.
+ *                  key, value, the caches and slot_mapping all NULL: only
+ *                  rotate q.
+ *   positions      int64 [num_axes][num_tokens]; num_axes 1 to 8 (1: text; 3:
+ *                  time, height and width of image and video tokens).
+ *   inv_freq       fp32 [rotary_dim / 2]: radians per position of each pair.
+ *   pair_axis      int32 [rotary_dim / 2]: the axis whose position turns each
+ *                  pair, in any assignment (sections, interleaved).  NULL:
+ *                  axis 0 for all.
+ *   rot_scale      factor on the rotated dims (1, or the attention factor of
+ *                  stretched frequencies).
+ * rotary_dim is a multiple of 16, at most head_dim; head_dim * element size,
+ * every stride * element size and every buffer are multiples of 16 bytes;
+ * any block_size >= 1.  Rows of different tokens must not overlap in q_out.
+ */
+typedef enum pa_rope_style {
+    PA_ROPE_HALVES = 0,
+    PA_ROPE_ADJACENT = 1
+} pa_rope_style;
+
+pa_status pa_rope_append(void *q_out, const void *q, const void *key, const void *value,
+                         void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                         const int64_t *positions, const float *inv_freq,
+                         const int32_t *pair_axis, int num_axes, int rotary_dim,
+                         pa_rope_style style, float rot_scale, int64_t q_out_stride,
+                         int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                         int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                         int block_size, int num_blocks, pa_dtype dtype, int32_t *err_flag,
+                         void *stream);
 
 /* ------------------------------------------------------------------------
  * Fused slot write + decode attention

@@ -34,6 +34,7 @@ static_assert(pa::kErrPair == PA_ERRBIT_PAIR, "error bit mismatch");
 static_assert(pa::kErrTimeout == PA_ERRBIT_TIMEOUT, "error bit mismatch");
 static_assert(pa::kErrQuery == PA_ERRBIT_QUERY, "error bit mismatch");
 static_assert(pa::kErrGroup == PA_ERRBIT_GROUP, "error bit mismatch");
+static_assert(pa::kErrAxis == PA_ERRBIT_AXIS, "error bit mismatch");
 
 namespace {
 
@@ -728,6 +729,77 @@ pa_status pa_reshape_and_cache(const void* key, const void* value, void* k_cache
       key, value, k_cache, v_cache, slot_mapping, num_tokens, num_kv_heads,
       static_cast<int>(row), block_size, static_cast<long long>(num_blocks) * block_size,
       err_flag, dev.sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status pa_rope_append(void* q_out, const void* q, const void* key, const void* value,
+                         void* k_cache, void* v_cache, const int64_t* slot_mapping,
+                         const int64_t* positions, const float* inv_freq,
+                         const int32_t* pair_axis, int num_axes, int rotary_dim,
+                         pa_rope_style style, float rot_scale, int64_t q_out_stride,
+                         int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                         int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                         int block_size, int num_blocks, pa_dtype dtype, int32_t* err_flag,
+                         void* stream) {
+  if (num_tokens < 0 || num_axes < 1 || num_axes > pa::kMaxRopeAxes || rotary_dim <= 0 ||
+      head_dim <= 0 || rotary_dim > head_dim || !std::isfinite(rot_scale) || !valid_dtype(dtype) ||
+      (style != PA_ROPE_HALVES && style != PA_ROPE_ADJACENT))
+    return PA_ERR_INVALID_ARG;
+  const int eb = elem_bytes(dtype);
+  if (static_cast<long long>(head_dim) * eb % 16 != 0) return PA_ERR_INVALID_ARG;
+  if (rotary_dim % 16 != 0 || head_dim > 4096) return PA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PA_OK;
+  const bool rotate = q || q_out, append = key || value || k_cache || v_cache || slot_mapping;
+  if (rotate && (num_q_heads <= 0 || !q || !q_out)) return PA_ERR_INVALID_ARG;
+  if (append && (num_kv_heads <= 0 || block_size <= 0 || num_blocks <= 0 || !key || !value ||
+                 !k_cache || !v_cache || !slot_mapping))
+    return PA_ERR_INVALID_ARG;
+  if (!rotate && !append) return PA_ERR_INVALID_ARG;
+  if ((rotate && num_q_heads > 0xffff) || (append && num_kv_heads > 0xffff))
+    return PA_ERR_UNSUPPORTED;
+  if (!positions || !inv_freq) return PA_ERR_INVALID_ARG;
+  // a row stride: whole 16-byte chunks, rows that do not overlap
+  auto bad_rows = [&](const void* p, int64_t stride, int heads) {
+    return !aligned16(p) || stride < 0 || stride % (16 / eb) != 0 ||
+           (num_tokens > 1 && stride < static_cast<int64_t>(heads) * head_dim);
+  };
+  if (rotate && (bad_rows(q, q_stride, num_q_heads) || bad_rows(q_out, q_out_stride, num_q_heads) ||
+                 (q == q_out && num_tokens > 1 && q_stride != q_out_stride)))
+    return PA_ERR_INVALID_ARG;
+  if (append && (bad_rows(key, key_stride, num_kv_heads) ||
+                 bad_rows(value, value_stride, num_kv_heads) || !aligned16(k_cache) ||
+                 !aligned16(v_cache)))
+    return PA_ERR_INVALID_ARG;
+  DeviceInfo dev;
+  const pa_status st = device_info(&dev);
+  if (st != PA_OK) return st;
+  pa::RopeArgs a{};
+  a.q = q;
+  a.q_out = q_out;
+  a.key = key;
+  a.value = value;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.inv_freq = inv_freq;
+  a.pair_axis = pair_axis;
+  a.num_axes = num_axes;
+  a.rotary_dim = rotary_dim;
+  a.rot_scale = rot_scale;
+  a.q_stride = q_stride;
+  a.key_stride = key_stride;
+  a.value_stride = value_stride;
+  a.q_out_stride = q_out_stride;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  a.block_size = block_size;
+  a.num_slots = append ? static_cast<long long>(num_blocks) * block_size : 0;
+  a.err_flag = err_flag;
+  const cudaError_t e = pa::launch_rope_append(a, eb, style == PA_ROPE_ADJACENT, dev.sms,
+                                               static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

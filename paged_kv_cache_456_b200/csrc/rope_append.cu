@@ -1,0 +1,253 @@
+// rope_append.cu -- rotary positions applied on the way into the paged cache.
+//
+// For token t, a q or k head row x and pair i of its rotary_dim / 2 rotated
+// pairs (a, b) = (x[i], x[i + rotary_dim / 2]) or (x[2 i], x[2 i + 1]):
+//   theta  = positions[axis(i)][t] * inv_freq[i]
+//   (a, b) <- rot_scale * (a cos theta - b sin theta, a sin theta + b cos theta)
+// Dims from rotary_dim on are copied.  A q row goes to q_out, a k row to its
+// cache slot, and the v row is copied to its slot beside it.
+//
+// Memory-bound: every row is read and written once, about 3 fp32 operations
+// an element.  What is not a stream is kept off it:
+//   * the angles.  A token's cos and sin are the same for all its heads, so a
+//     CTA computes them once into shared memory, rotary_dim / 2 per token.
+//     theta is formed and reduced in fp64 (positions of a million times
+//     frequencies near 1 leave fp32 with no fraction), as a fraction of a
+//     turn, which sincospif takes in fp32: |error| < 1e-7.
+//   * the slots: one division per token, not per element.
+// A thread's unit of work is two 16-byte chunks of one row: the two halves of
+// the same 8 (bf16) or 4 (fp32) pairs, or two chunks to copy.  The units of a
+// CTA's tokens are laid end to end (q heads, k heads, v heads), consecutive
+// threads on consecutive chunks.  The first units' rows are requested before
+// the angles are computed, which hides the one behind the other.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "pa_internal.h"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnitsAhead = 2;  // units a thread has in flight
+constexpr size_t kMaxSmem = 40 * 1024;
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f32(float x, float* y) { *y = x; }
+__device__ __forceinline__ void from_f32(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
+
+template <typename T>
+union Chunk {
+  uint4 v;
+  T e[16 / sizeof(T)];
+};
+
+// One unit of work: two chunks of one row (the second missing where c1 < 0).
+struct Unit {
+  int tok = -1;   // token within the CTA (-1: no unit)
+  int part;       // 0: q, 1: key, 2: value
+  int head;
+  int c0, c1;     // chunks of the row
+  bool rotated;
+};
+
+template <typename T, bool ADJACENT>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a) {
+  constexpr int VE = 16 / sizeof(T);
+  extern __shared__ float smem[];
+  const int tpc = a.tokens_per_cta, half = a.rotary_dim / 2;
+  float* const s_cos = smem;               // [tpc][half]
+  float* const s_sin = s_cos + tpc * half;
+  long long* const s_row = reinterpret_cast<long long*>(s_sin + tpc * half);  // [tpc]
+  const int tid = threadIdx.x;
+  const long long t0 = static_cast<long long>(blockIdx.x) * tpc;
+  const int nt = static_cast<int>(a.num_tokens - t0 < tpc ? a.num_tokens - t0 : tpc);
+
+  // units of a row: rotated ones, then the copied rest two chunks at a time
+  const int chunks = a.head_dim / VE;
+  const int ur = a.rotary_dim / (2 * VE);
+  const int rest = chunks - 2 * ur, uc = (rest + 1) / 2;
+  const int uv = (chunks + 1) / 2;
+  const int uq = ur + uc;
+  const int nq = a.q ? a.num_q_heads * uq : 0;
+  const int nk = a.key ? a.num_kv_heads * uq : 0;
+  const int nv = a.key ? a.num_kv_heads * uv : 0;
+  const int per_token = nq + nk + nv;
+  const int begin = blockIdx.y * a.units_per_slice;
+  const int end = min(nt * per_token, begin + a.units_per_slice);
+
+  // the slots first: the copies' addresses need them
+  if (tid < nt) {
+    long long row = -1;
+    if (a.key) {
+      const long long slot = a.slot_mapping[t0 + tid];
+      if (slot >= a.num_slots) {
+        if (blockIdx.y == 0 && a.err_flag) atomicOr(a.err_flag, kErrSlot);
+      } else if (slot >= 0) {
+        const long long blk = slot / a.block_size;
+        row = blk * a.num_kv_heads * a.block_size + (slot - blk * a.block_size);
+      }
+    }
+    s_row[tid] = row;
+  }
+
+  auto locate = [&](int i) -> Unit {
+    Unit u;
+    if (i >= end) return u;
+    u.tok = i / per_token;
+    int r = i - u.tok * per_token;
+    u.part = r < nq ? 0 : r < nq + nk ? 1 : 2;
+    r -= u.part == 0 ? 0 : u.part == 1 ? nq : nq + nk;
+    const int width = u.part == 2 ? uv : uq;
+    u.head = r / width;
+    const int w = r - u.head * width;
+    u.rotated = u.part != 2 && w < ur;
+    if (u.rotated) {
+      u.c0 = w;
+      u.c1 = w + ur;
+    } else {  // the n chunks from `first` on, the two halves of them side by side
+      const int first = u.part == 2 ? 0 : 2 * ur, n = chunks - first, k = u.part == 2 ? w : w - ur;
+      u.c0 = first + k;
+      u.c1 = k + (n + 1) / 2 < n ? u.c0 + (n + 1) / 2 : -1;
+    }
+    return u;
+  };
+  auto source = [&](const Unit& u) -> const uint4* {
+    const void* p = u.part == 0 ? a.q : u.part == 1 ? a.key : a.value;
+    const long long stride = u.part == 0 ? a.q_stride : u.part == 1 ? a.key_stride : a.value_stride;
+    return reinterpret_cast<const uint4*>(static_cast<const T*>(p) + (t0 + u.tok) * stride +
+                                          static_cast<long long>(u.head) * a.head_dim);
+  };
+  // (after the barrier: the slots are in shared memory; null: a padding token)
+  auto destination = [&](const Unit& u) -> uint4* {
+    if (u.part == 0)
+      return reinterpret_cast<uint4*>(static_cast<T*>(a.q_out) + (t0 + u.tok) * a.q_out_stride +
+                                      static_cast<long long>(u.head) * a.head_dim);
+    const long long row = s_row[u.tok];
+    if (row < 0) return nullptr;
+    T* const cache = static_cast<T*>(u.part == 1 ? a.k_cache : a.v_cache);
+    return reinterpret_cast<uint4*>(cache + (row + static_cast<long long>(u.head) * a.block_size) *
+                                                a.head_dim);
+  };
+
+  Unit u[kUnitsAhead];
+  Chunk<T> x0[kUnitsAhead], x1[kUnitsAhead];
+  auto load = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < kUnitsAhead; ++k) {
+      u[k] = locate(i + k * kThreads);
+      if (u[k].tok >= 0) {
+        const uint4* const src = source(u[k]);
+        x0[k].v = src[u[k].c0];
+        if (u[k].c1 >= 0) x1[k].v = src[u[k].c1];
+      }
+    }
+  };
+  load(begin + tid);
+
+  // the angles of this CTA's tokens
+  for (int i = tid; i < nt * half; i += kThreads) {
+    const int tok = i / half, p = i - tok * half;
+    int axis = 0;
+    if (a.pair_axis) {
+      axis = a.pair_axis[p];
+      if (axis < 0 || axis >= a.num_axes) {
+        if (a.err_flag) atomicOr(a.err_flag, kErrAxis);
+        axis = -1;
+      }
+    }
+    float c = a.rot_scale, s = 0.f;  // (a pair without an axis is not turned)
+    if (axis >= 0) {
+      const double pos = static_cast<double>(a.positions[axis * a.num_tokens + t0 + tok]);
+      const double turns = pos * static_cast<double>(a.inv_freq[p]) * 0.15915494309189533577;
+      sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
+      c *= a.rot_scale;
+      s *= a.rot_scale;
+    }
+    s_cos[i] = c;
+    s_sin[i] = s;
+  }
+  __syncthreads();
+
+  for (int i = begin + tid; i < end; i += kUnitsAhead * kThreads) {
+    if (i != begin + tid) load(i);
+#pragma unroll
+    for (int k = 0; k < kUnitsAhead; ++k) {
+      if (u[k].tok < 0) continue;
+      if (u[k].rotated) {
+        const int p0 = u[k].tok * half;
+        if constexpr (ADJACENT) {
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            Chunk<T>& x = n ? x1[k] : x0[k];
+            const int p = p0 + (n ? u[k].c1 : u[k].c0) * (VE / 2);
+#pragma unroll
+            for (int j = 0; j < VE / 2; ++j) {
+              const float c = s_cos[p + j], s = s_sin[p + j];
+              const float xa = to_f32(x.e[2 * j]), xb = to_f32(x.e[2 * j + 1]);
+              from_f32(fmaf(xa, c, -(xb * s)), &x.e[2 * j]);
+              from_f32(fmaf(xa, s, xb * c), &x.e[2 * j + 1]);
+            }
+          }
+        } else {
+          const int p = p0 + u[k].c0 * VE;
+#pragma unroll
+          for (int j = 0; j < VE; ++j) {
+            const float c = s_cos[p + j], s = s_sin[p + j];
+            const float xa = to_f32(x0[k].e[j]), xb = to_f32(x1[k].e[j]);
+            from_f32(fmaf(xa, c, -(xb * s)), &x0[k].e[j]);
+            from_f32(fmaf(xa, s, xb * c), &x1[k].e[j]);
+          }
+        }
+      }
+      uint4* const dst = destination(u[k]);
+      if (dst) {
+        dst[u[k].c0] = x0[k].v;
+        if (u[k].c1 >= 0) dst[u[k].c1] = x1[k].v;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+// Launch shape.  A CTA takes as many tokens as give each thread about four
+// units, so that a token's angles serve many rows; where that leaves fewer
+// CTAs than fill the GPU twice, the units of one token are cut into slices of
+// one unit per thread instead (each slice computes the token's angles again:
+// with so few tokens that costs no bandwidth, only a few hundred cycles that
+// the rows' own loads cover).
+cudaError_t launch_rope_append(RopeArgs a, int elem_bytes, bool adjacent, int num_sms,
+                               cudaStream_t stream) {
+  const int ve = 16 / elem_bytes;
+  const int chunks = a.head_dim / ve, ur = a.rotary_dim / (2 * ve);
+  const int uq = ur + (chunks - 2 * ur + 1) / 2, uv = (chunks + 1) / 2;
+  const long long per_token = (a.q ? static_cast<long long>(a.num_q_heads) * uq : 0) +
+                              (a.key ? static_cast<long long>(a.num_kv_heads) * (uq + uv) : 0);
+  const size_t token_smem = a.rotary_dim * sizeof(float) + sizeof(long long);
+  long long tpc = std::min<long long>({4 * kThreads / per_token, kThreads,
+                                       static_cast<long long>(kMaxSmem / token_smem)});
+  if (tpc < 1) tpc = 1;
+  long long slice = per_token * tpc;
+  if ((a.num_tokens + tpc - 1) / tpc < 2LL * num_sms) {
+    tpc = 1;
+    slice = std::max<long long>(kThreads, (per_token + 65534) / 65535);
+  }
+  const long long slices = (per_token * tpc + slice - 1) / slice;
+  a.tokens_per_cta = static_cast<int>(tpc);
+  a.units_per_slice = static_cast<int>(slice);
+  const size_t smem = static_cast<size_t>(tpc) * token_smem;
+  const dim3 grid(static_cast<unsigned>((a.num_tokens + tpc - 1) / tpc), static_cast<unsigned>(slices));
+  auto go = [&](auto kernel) { kernel<<<grid, kThreads, smem, stream>>>(a); };
+  if (elem_bytes == 2)
+    adjacent ? go(rope_append_kernel<__nv_bfloat16, true>) : go(rope_append_kernel<__nv_bfloat16, false>);
+  else
+    adjacent ? go(rope_append_kernel<float, true>) : go(rope_append_kernel<float, false>);
+  return cudaGetLastError();
+}
+
+}  // namespace pa

@@ -29,13 +29,14 @@ ERRBIT_PAIR = 8
 ERRBIT_TIMEOUT = 16
 ERRBIT_QUERY = 32
 ERRBIT_GROUP = 64
+ERRBIT_AXIS = 128
 
 EXPORTED = ("pa_status_str", "pa_decode_workspace_size", "pa_decode_workspace_init",
             "pa_decode_launch_config", "pa_decode", "pa_decode_noalloc", "pa_decode_append",
             "pa_prefill", "pa_prefill_workspace_size", "pa_prefill_launch_config",
             "pa_reshape_and_cache", "pa_copy_blocks", "pa_shared_prefix_plan",
             "pa_shared_prefix_plan_tree",
-            "pa_shared_prefix_workspace_size", "pa_decode_shared_prefix")
+            "pa_shared_prefix_workspace_size", "pa_decode_shared_prefix", "pa_rope_append")
 
 # size of the library's fixed scratch array used by pa_decode_noalloc
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -85,6 +86,9 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.pa_reshape_and_cache.restype = i
     lib.pa_copy_blocks.argtypes = [vp] * 3 + [i] * 6 + [vp, vp]
     lib.pa_copy_blocks.restype = i
+    i64 = ctypes.c_int64
+    lib.pa_rope_append.argtypes = [vp] * 10 + [i] * 3 + [f] + [i64] * 4 + [i] * 7 + [vp, vp]
+    lib.pa_rope_append.restype = i
     ip = ctypes.POINTER(i)
     lib.pa_shared_prefix_plan.argtypes = [vp, vp] + [i] * 4 + [vp, vp, vp, ip, ip]
     lib.pa_shared_prefix_plan.restype = i
@@ -128,6 +132,35 @@ def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _same_device(ref: torch.Tensor, **others: Optional[torch.Tensor]) -> None:
+    """Every tensor on ``ref``'s CUDA device (a host pointer would fault in the kernel)."""
+    dev = ref.device
+    if dev.type != "cuda":
+        raise ValueError("libpa works on CUDA tensors")
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+
+
+def _rows_ptr(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype):
+    """(pointer, elements between tokens) of ``[T][H][D]`` rows whose heads lie side by side."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
+                         f"not {t.dtype} of shape {tuple(t.shape)}")
+    T, H, D = shape
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), st[0] if T > 1 else H * D
+
+
+def _array_ptr(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> int:
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)}, "
+                         f"not {t.dtype} of shape {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 # ---------------------------------------------------------------------------
@@ -272,6 +305,63 @@ def reshape_and_cache(key: torch.Tensor, value: torch.Tensor, k_cache: torch.Ten
     _check(library().pa_reshape_and_cache(
         _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), T, Hkv, D, bs, N,
         _dtype_code(k_cache), _ptr(err_flag), _stream(stream)), "pa_reshape_and_cache")
+
+
+def rope_append(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
+                key: Optional[torch.Tensor], value: Optional[torch.Tensor],
+                k_cache: Optional[torch.Tensor], v_cache: Optional[torch.Tensor],
+                slot_mapping: Optional[torch.Tensor], positions: torch.Tensor,
+                inv_freq: torch.Tensor, *, pair_axis: Optional[torch.Tensor] = None,
+                adjacent: bool = False, rot_scale: float = 1.0,
+                err_flag: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """Turn ``q`` ``[T][Hq][D]`` by the tokens' positions into ``q_out`` and write the
+    turned ``key`` and the ``value`` ``[T][Hkv][D]`` into their cache slots; see
+    ``pa_rope_append``.  ``positions`` is int64 ``[T]`` or ``[axes][T]``; ``2 *
+    len(inv_freq)`` dims of a head are turned, in pairs of its two halves, or of
+    neighbours with ``adjacent``.  ``q``/``q_out`` may be one tensor, or both None;
+    ``key`` to ``slot_mapping`` may all be None.  q, q_out, key and value may be
+    views whose tokens lie apart."""
+    ref = q if q is not None else key
+    if ref is None:
+        raise ValueError("rope_append needs q or key")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    append = (key, value, k_cache, v_cache, slot_mapping)
+    if any(t is None for t in append) and any(t is not None for t in append):
+        raise ValueError("key, value, k_cache, v_cache and slot_mapping go together")
+    if ref.dim() != 3:
+        raise ValueError("q and key are [tokens][heads][head_dim]")
+    _same_device(ref, q_out=q_out, key=key, value=value, k_cache=k_cache, v_cache=v_cache,
+                 slot_mapping=slot_mapping, positions=positions, inv_freq=inv_freq,
+                 pair_axis=pair_axis, err_flag=err_flag)
+    T, _, D = ref.shape
+    dt = ref.dtype
+    code = _dtype_code(ref)
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    half = inv_freq.numel()
+    pos = _array_ptr("positions", positions, (T,) if positions.dim() == 1 else (axes, T), torch.int64)
+    freq = _array_ptr("inv_freq", inv_freq, (half,), torch.float32)
+    axis = None if pair_axis is None else _array_ptr("pair_axis", pair_axis, (half,), torch.int32)
+    qp = qs = op = os_ = kp = ks = vp = vs = kc = vc = slots = Hq = Hkv = N = 0
+    bs = 1
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _rows_ptr("q", q, (T, Hq, D), dt)
+        op, os_ = _rows_ptr("q_out", q_out, (T, Hq, D), dt)
+    if key is not None:
+        N, Hkv, bs, _ = k_cache.shape
+        kp, ks = _rows_ptr("key", key, (T, Hkv, D), dt)
+        vp, vs = _rows_ptr("value", value, (T, Hkv, D), dt)
+        kc = _array_ptr("k_cache", k_cache, (N, Hkv, bs, D), dt)
+        vc = _array_ptr("v_cache", v_cache, (N, Hkv, bs, D), dt)
+        slots = _array_ptr("slot_mapping", slot_mapping, (T,), torch.int64)
+    err = None if err_flag is None else _array_ptr("err_flag", err_flag, err_flag.shape, torch.int32)
+    with torch.cuda.device(ref.device):
+        _check(library().pa_rope_append(
+            op, qp, kp, vp, kc, vc, slots, pos, freq, axis, axes, 2 * half, int(adjacent),
+            rot_scale, os_, qs, ks, vs, T, Hq, Hkv, D, bs, N, code, err, _stream(stream)),
+            "pa_rope_append")
+    return q_out
 
 
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, block_mapping: torch.Tensor,
