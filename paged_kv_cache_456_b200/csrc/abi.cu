@@ -15,6 +15,7 @@
 
 #include "paged_attention.h"
 #include "pa_internal.h"
+#include "rope_append.h"
 
 namespace pa {
 cudaError_t launch_reshape_and_cache(const void* key, const void* value, void* k_cache,

@@ -27,6 +27,7 @@
 #include <cuda_runtime.h>
 
 #include "pa_internal.h"
+#include "rope_append.h"
 
 namespace pa {
 namespace {
