@@ -355,6 +355,52 @@ pa_status pa_prefill(void *out, const void *q, const void *k_cache, const void *
                      size_t workspace_bytes, int32_t *err_flag, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Cross attention (all tokens, any number of rows)
+ * ------------------------------------------------------------------------
+ * pa_prefill without the causal order: the query rows of sequence s attend
+ * to ALL n = context_lens[s] tokens that block_tables[s] lists -- an
+ * encoder's states, a document, the context of candidates to be ranked --
+ * whose number has nothing to do with the number of rows
+ * Q = query_start[s+1] - query_start[s].  For every row r of sequence s and
+ * query head h, with K_i, V_i of KV head h / (num_q_heads / num_kv_heads):
+ *     out[r][h][:] = softmax_i(scale * q[r][h] . K_i) . V_i,  i = 0 .. n-1
+ * n == 0 gives zero rows.  The states are written to the cache once, with
+ * pa_reshape_and_cache (or pa_rope_append), and read by every later step:
+ * one row per sequence while generating, many rows for a prompt or an image.
+ *
+ *   q, out          device, [num_query_tokens][num_q_heads][head_dim].
+ *   query_start     device int32 [num_seqs + 1], non-decreasing, values in
+ *                   [0, num_query_tokens].  Rows before query_start[0] and
+ *                   from query_start[num_seqs] on are not touched.  A
+ *                   sequence whose pair is out of order or out of range sets
+ *                   PA_ERRBIT_QUERY; its rows may be left unwritten.
+ *   context_lens    a length outside [0, min(max_context_len,
+ *                   max_blocks_per_seq * 16)] sets PA_ERRBIT_CONTEXT_LEN, a
+ *                   block id outside the cache among the blocks attended to
+ *                   sets PA_ERRBIT_BLOCK_ID: that sequence's rows are written
+ *                   as zeros.  (A sequence without rows is not checked.)
+ *   workspace       pa_cross_attention_workspace_size() bytes, 16-byte
+ *                   aligned; its contents on entry do not matter.  Two calls
+ *                   that may run at the same time must not share one.
+ *   Everything else, and the supported shapes, are as in pa_decode.
+ *
+ * fp32 caches: fp32 arithmetic throughout.  The work is cut into equal
+ * shares whatever the lengths, a split row's parts being merged exactly (up
+ * to rounding); repeated calls give the same bits.
+ */
+pa_status pa_cross_attention_workspace_size(int num_seqs, int num_query_tokens, int num_q_heads,
+                                            int num_kv_heads, int head_dim, int max_context_len,
+                                            pa_dtype dtype, size_t *bytes);
+
+pa_status pa_cross_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                             const int32_t *block_tables, const int32_t *context_lens,
+                             const int32_t *query_start, int num_seqs, int num_query_tokens,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             int max_blocks_per_seq, int num_blocks, int max_context_len,
+                             float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes,
+                             int32_t *err_flag, void *stream);
+
+/* ------------------------------------------------------------------------
  * Prefix-deduplicated decode
  * ------------------------------------------------------------------------
  * Requests with a common prefix hold the same physical blocks for it

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include "paged_attention.h"
+#include "cross_attention.h"
 #include "pa_internal.h"
 #include "rope_append.h"
 
@@ -802,6 +803,113 @@ pa_status pa_rope_append(void* q_out, const void* q, const void* key, const void
   const cudaError_t e = pa::launch_rope_append(a, eb, style == PA_ROPE_ADJACENT, dev.sms,
                                                static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+namespace {
+
+// Shape checks of pa_cross_attention that need no device, and its plan.
+pa_status cross_shape(int num_seqs, int num_query_tokens, int num_q_heads, int num_kv_heads,
+                      int head_dim, int max_context_len, pa_dtype dtype) {
+  if (num_query_tokens < 0) return PA_ERR_INVALID_ARG;
+  const pa_status st =
+      check_decode_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, 0, dtype);
+  if (st != PA_OK) return st;
+  // columns are numbered in 32 bits
+  if (static_cast<long long>(num_query_tokens) * num_q_heads >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
+  return PA_OK;
+}
+
+}  // namespace
+
+pa_status pa_cross_attention_workspace_size(int num_seqs, int num_query_tokens, int num_q_heads,
+                                            int num_kv_heads, int head_dim, int max_context_len,
+                                            pa_dtype dtype, size_t* bytes) {
+  if (!bytes) return PA_ERR_INVALID_ARG;
+  pa_status st = cross_shape(num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim,
+                             max_context_len, dtype);
+  if (st != PA_OK) return st;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != PA_OK) return st;
+  *bytes = pa::cross_plan(num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim,
+                          elem_bytes(dtype), dev.sms)
+               .bytes;
+  return PA_OK;
+}
+
+pa_status pa_cross_attention(void* out, const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, const int32_t* context_lens,
+                             const int32_t* query_start, int num_seqs, int num_query_tokens,
+                             int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                             int max_blocks_per_seq, int num_blocks, int max_context_len,
+                             float scale, pa_dtype dtype, void* workspace, size_t workspace_bytes,
+                             int32_t* err_flag, void* stream) {
+  pa_status st = cross_shape(num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim,
+                             max_context_len, dtype);
+  if (st != PA_OK) return st;
+  if (max_blocks_per_seq <= 0 || num_blocks <= 0 || block_size <= 0 || !std::isfinite(scale))
+    return PA_ERR_INVALID_ARG;
+  if (block_size != pa::kBlockSize) return PA_ERR_UNSUPPORTED;
+  if (num_query_tokens == 0) return PA_OK;
+  if (num_seqs == 0) return PA_ERR_INVALID_ARG;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start)
+    return PA_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PA_ERR_INVALID_ARG;
+  // tensor loads take 32-bit row numbers of the [num_blocks * Hkv * 16][head_dim] view
+  const long long rows = static_cast<long long>(num_blocks) * num_kv_heads * pa::kBlockSize;
+  if (dtype == PA_BF16 && rows + pa::kBlockSize >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
+  const long long cap = static_cast<long long>(max_blocks_per_seq) * pa::kBlockSize;
+  const long long len_cap = max_context_len < cap ? max_context_len : cap;
+  if (len_cap > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  DeviceInfo dev;
+  if ((st = device_info(&dev)) != PA_OK) return st;
+  const pa::CrossPlan p = pa::cross_plan(num_seqs, num_query_tokens, num_q_heads, num_kv_heads,
+                                         head_dim, elem_bytes(dtype), dev.sms);
+  // a worker's share of the tiles is counted in 32 bits
+  const long long groups =
+      static_cast<long long>(num_query_tokens) * (num_q_heads / num_kv_heads) / p.cols + num_seqs;
+  if (groups * num_kv_heads >= (1LL << 36) / (len_cap / p.keys + 1)) return PA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < p.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+
+  pa::CrossArgs a{};
+  a.q = q;
+  a.out = out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.query_start = query_start;
+  a.num_seqs = num_seqs;
+  a.num_rows = num_query_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.head_dim = head_dim;
+  while ((num_kv_heads << a.group_log2) < num_q_heads) ++a.group_log2;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = num_blocks;
+  a.len_cap = static_cast<int>(len_cap);
+  a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  a.err_flag = err_flag;
+  a.cols = p.cols;
+  a.keys = p.keys;
+  a.max_workers = p.max_workers;
+  a.min_tiles = p.min_tiles;
+  char* const ws = static_cast<char*>(workspace);
+  a.head = reinterpret_cast<long long*>(ws);
+  a.rec = reinterpret_cast<int4*>(ws + p.rec_off);
+  a.meta = reinterpret_cast<int4*>(ws + p.meta_off);
+  a.start = reinterpret_cast<long long*>(ws + p.start_off);
+  a.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
+  a.part_o = reinterpret_cast<float*>(ws + p.o_off);
+  if (dtype == PA_BF16 && ((st = encode_cache_map(&a.tm_k, k_cache, rows, head_dim)) != PA_OK ||
+                           (st = encode_cache_map(&a.tm_v, v_cache, rows, head_dim)) != PA_OK))
+    return st;
+  if (pa::launch_cross_attention(a, elem_bytes(dtype), dev.sms, static_cast<cudaStream_t>(stream)) !=
+      cudaSuccess) {
+    cudaGetLastError();
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
 }
 
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_mapping,

@@ -36,7 +36,8 @@ EXPORTED = ("pa_status_str", "pa_decode_workspace_size", "pa_decode_workspace_in
             "pa_prefill", "pa_prefill_workspace_size", "pa_prefill_launch_config",
             "pa_reshape_and_cache", "pa_copy_blocks", "pa_shared_prefix_plan",
             "pa_shared_prefix_plan_tree",
-            "pa_shared_prefix_workspace_size", "pa_decode_shared_prefix", "pa_rope_append")
+            "pa_shared_prefix_workspace_size", "pa_decode_shared_prefix", "pa_rope_append",
+            "pa_cross_attention", "pa_cross_attention_workspace_size")
 
 # size of the library's fixed scratch array used by pa_decode_noalloc
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
@@ -89,6 +90,10 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
     i64 = ctypes.c_int64
     lib.pa_rope_append.argtypes = [vp] * 10 + [i] * 3 + [f] + [i64] * 4 + [i] * 7 + [vp, vp]
     lib.pa_rope_append.restype = i
+    lib.pa_cross_attention_workspace_size.argtypes = [i] * 7 + [ctypes.POINTER(sz)]
+    lib.pa_cross_attention_workspace_size.restype = i
+    lib.pa_cross_attention.argtypes = [vp] * 7 + [i] * 9 + [f, i, vp, sz, vp, vp]
+    lib.pa_cross_attention.restype = i
     ip = ctypes.POINTER(i)
     lib.pa_shared_prefix_plan.argtypes = [vp, vp] + [i] * 4 + [vp, vp, vp, ip, ip]
     lib.pa_shared_prefix_plan.restype = i
@@ -274,6 +279,57 @@ def prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         int(max_context_len), float(scale), int(partition_size), _dtype_code(q),
         _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(err_flag),
         _stream(stream)), "pa_prefill")
+    return out
+
+
+def make_cross_attention_workspace(num_seqs: int, num_query_tokens: int, num_q_heads: int,
+                                   num_kv_heads: int, head_dim: int, max_context_len: int,
+                                   dtype: torch.dtype = torch.bfloat16, device="cuda") -> torch.Tensor:
+    """A workspace of the size ``pa_cross_attention`` needs for these sizes (its contents do
+    not matter)."""
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(device):
+        _check(library().pa_cross_attention_workspace_size(
+            num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim, int(max_context_len),
+            PA_BF16 if dtype == torch.bfloat16 else PA_F32, ctypes.byref(n)),
+            "pa_cross_attention_workspace_size")
+    return torch.empty(max(n.value, 16), dtype=torch.uint8, device=device)
+
+
+def cross_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                    v_cache: torch.Tensor, block_tables: torch.Tensor,
+                    context_lens: torch.Tensor, query_start: torch.Tensor, *, scale: float,
+                    max_context_len: int, workspace: torch.Tensor,
+                    err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of each sequence's rows of ``q`` ``[T][Hq][D]`` (rows ``query_start[s]`` to
+    ``query_start[s+1]``) to all ``context_lens[s]`` tokens of its block table, into ``out``;
+    see ``pa_cross_attention``."""
+    _same_device(q, out=out, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+                 context_lens=context_lens, query_start=query_start, workspace=workspace,
+                 err_flag=err_flag)
+    if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("q is [rows][heads][head_dim], the caches [blocks][heads][16][head_dim], "
+                         "block_tables [sequences][blocks]")
+    T, Hq, D = q.shape
+    N, Hkv, bs, _ = k_cache.shape
+    S, B = block_tables.shape
+    dt = q.dtype
+    code = _dtype_code(q)
+    i32 = torch.int32
+    args = (_array_ptr("out", out, (T, Hq, D), dt), _array_ptr("q", q, (T, Hq, D), dt),
+            _array_ptr("k_cache", k_cache, (N, Hkv, bs, D), dt),
+            _array_ptr("v_cache", v_cache, (N, Hkv, bs, D), dt),
+            _array_ptr("block_tables", block_tables, (S, B), i32),
+            _array_ptr("context_lens", context_lens, (S,), i32),
+            _array_ptr("query_start", query_start, (S + 1,), i32))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    err = None if err_flag is None else _array_ptr("err_flag", err_flag, err_flag.shape, i32)
+    with torch.cuda.device(q.device):
+        _check(library().pa_cross_attention(
+            *args, S, T, Hq, Hkv, D, bs, B, N, int(max_context_len), scale, code,
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), err,
+            _stream(stream)), "pa_cross_attention")
     return out
 
 
