@@ -216,6 +216,7 @@ std::map<std::pair<int, const void*>, size_t> g_smem;  // (device, kernel) -> li
 }  // namespace
 
 CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes) {
+  if (elem_bytes == 2) return cross_tc_kernel_info(head_dim);
   return cross_simt_kernel_info(head_dim, elem_bytes);
 }
 

@@ -19,4 +19,7 @@ CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, in
 // fp32 arithmetic on the CUDA cores (cross_simt.cu)
 CrossKernel cross_simt_kernel_info(int head_dim, int elem_bytes);
 
+// bf16, many columns: tcgen05 tensor cores (cross_tc.cu)
+CrossKernel cross_tc_kernel_info(int head_dim);
+
 }  // namespace pa
