@@ -380,8 +380,10 @@ pa_status pa_prefill(void *out, const void *q, const void *k_cache, const void *
  *                   sets PA_ERRBIT_BLOCK_ID: that sequence's rows are written
  *                   as zeros.  (A sequence without rows is not checked.)
  *   workspace       pa_cross_attention_workspace_size() bytes, 16-byte
- *                   aligned; its contents on entry do not matter.  Two calls
- *                   that may run at the same time must not share one.
+ *                   aligned, zero-filled once before its first use
+ *                   (pa_decode_workspace_init); every call leaves it ready
+ *                   for the next, of whatever sizes.  Two calls that may run
+ *                   at the same time must not share one.
  *   Everything else, and the supported shapes, are as in pa_decode.
  *
  * fp32 caches: fp32 arithmetic throughout.  The work is cut into equal

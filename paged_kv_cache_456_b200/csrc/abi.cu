@@ -814,8 +814,9 @@ pa_status cross_shape(int num_seqs, int num_query_tokens, int num_q_heads, int n
   const pa_status st =
       check_decode_shape(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, 0, dtype);
   if (st != PA_OK) return st;
-  // columns are numbered in 32 bits
-  if (static_cast<long long>(num_query_tokens) * num_q_heads >= (1LL << 31)) return PA_ERR_UNSUPPORTED;
+  // columns are numbered in 32 bits, elements of a group of columns too
+  if (static_cast<long long>(num_query_tokens) * num_q_heads >= (1LL << 31) || num_q_heads > 32768)
+    return PA_ERR_UNSUPPORTED;
   return PA_OK;
 }
 
@@ -830,8 +831,9 @@ pa_status pa_cross_attention_workspace_size(int num_seqs, int num_query_tokens, 
   if (st != PA_OK) return st;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != PA_OK) return st;
-  *bytes = pa::cross_plan(num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim,
-                          elem_bytes(dtype), dev.sms)
+  *bytes = pa::cross_layout(pa::cross_kernel(num_seqs, num_query_tokens, num_q_heads / num_kv_heads,
+                                             head_dim, elem_bytes(dtype)),
+                            head_dim, dev.sms)
                .bytes;
   return PA_OK;
 }
@@ -863,12 +865,13 @@ pa_status pa_cross_attention(void* out, const void* q, const void* k_cache, cons
   if (len_cap > (1 << 30)) return PA_ERR_UNSUPPORTED;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != PA_OK) return st;
-  const pa::CrossPlan p = pa::cross_plan(num_seqs, num_query_tokens, num_q_heads, num_kv_heads,
-                                         head_dim, elem_bytes(dtype), dev.sms);
+  const pa::CrossKernel k = pa::cross_kernel(num_seqs, num_query_tokens, num_q_heads / num_kv_heads,
+                                             head_dim, elem_bytes(dtype));
+  const pa::CrossLayout p = pa::cross_layout(k, head_dim, dev.sms);
   // a worker's share of the tiles is counted in 32 bits
   const long long groups =
-      static_cast<long long>(num_query_tokens) * (num_q_heads / num_kv_heads) / p.cols + num_seqs;
-  if (groups * num_kv_heads >= (1LL << 36) / (len_cap / p.keys + 1)) return PA_ERR_UNSUPPORTED;
+      static_cast<long long>(num_query_tokens) * (num_q_heads / num_kv_heads) / k.cols + num_seqs;
+  if (groups * num_kv_heads >= (1LL << 36) / (len_cap / k.keys + 1)) return PA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
 
   pa::CrossArgs a{};
@@ -883,29 +886,20 @@ pa_status pa_cross_attention(void* out, const void* q, const void* k_cache, cons
   a.num_rows = num_query_tokens;
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = num_kv_heads;
-  a.head_dim = head_dim;
   while ((num_kv_heads << a.group_log2) < num_q_heads) ++a.group_log2;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = num_blocks;
   a.len_cap = static_cast<int>(len_cap);
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   a.err_flag = err_flag;
-  a.cols = p.cols;
-  a.keys = p.keys;
-  a.max_workers = p.max_workers;
-  a.min_tiles = p.min_tiles;
   char* const ws = static_cast<char*>(workspace);
-  a.head = reinterpret_cast<long long*>(ws);
-  a.rec = reinterpret_cast<int4*>(ws + p.rec_off);
-  a.meta = reinterpret_cast<int4*>(ws + p.meta_off);
-  a.start = reinterpret_cast<long long*>(ws + p.start_off);
+  a.count = reinterpret_cast<unsigned*>(ws);
   a.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
   a.part_o = reinterpret_cast<float*>(ws + p.o_off);
   if (dtype == PA_BF16 && ((st = encode_cache_map(&a.tm_k, k_cache, rows, head_dim)) != PA_OK ||
                            (st = encode_cache_map(&a.tm_v, v_cache, rows, head_dim)) != PA_OK))
     return st;
-  if (pa::launch_cross_attention(a, elem_bytes(dtype), dev.sms, static_cast<cudaStream_t>(stream)) !=
-      cudaSuccess) {
+  if (pa::launch_cross_attention(a, k, dev.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return PA_ERR_CUDA;
   }

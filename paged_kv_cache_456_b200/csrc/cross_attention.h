@@ -1,26 +1,34 @@
 // cross_attention.h -- what the kernels of pa_cross_attention share: the
-// arguments, the work's layout in the workspace, and the walk over a worker's
-// share of it.
+// arguments, the cut of the work over the CTAs, and the merge of what it cuts.
 //
-// An item is (sequence, KV head, group of `cols` query columns); a column is
-// one (query row, query head) pair of the KV head, column c of a sequence
-// being row c / G, head c % G.  An item's keys are cut into tiles of `keys`;
-// an item without keys counts one tile (its rows are written as zeros).  All
-// tiles are laid end to end in (sequence, KV head, group, tile) order and cut
-// into equal contiguous shares, one per worker, so every worker gets the same
-// number of tiles however skewed the lengths are.  The run of one item's
-// tiles inside a share is a piece: a piece that is the whole item stores the
-// output, any other stores a partial state (m, l, o) for the merge kernel:
+// An item is (sequence, KV head, group of query columns); a column is one
+// (query row, query head) pair of the KV head, column c of a sequence being
+// row c / G, head c % G.  An item's keys are cut into tiles; an item without
+// keys counts one tile (its rows are written as zeros).  All tiles are laid
+// end to end in (sequence, KV head, group, tile) order and cut into equal
+// contiguous shares, one per worker (a CTA), so every CTA gets the same number
+// of tiles however skewed the lengths are.  The run of one item's tiles inside
+// a share is a piece: a piece that is the whole item stores the output, any
+// other stores a partial state (m, l, o), and the CTA that stores the last of
+// an item's partials merges them, in the order of the keys:
 //   M = max_j m_j,  out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
-// A worker has at most two partial pieces, hence two partial slots: slot 2 w
-// for the piece its share begins inside of, 2 w + 1 for the one it begins and
-// does not finish.  Nothing in the workspace outlives a call or needs zeroing.
+// No CTA waits for another.  A worker has at most two partial pieces, hence
+// two slots: slot 2 w for the piece its share begins inside of, 2 w + 1 for
+// the one it begins and does not finish.
+//
+// Every CTA lays the work out for itself (cross_share): that costs it one
+// round of loads and a scan, less than a launch ahead of it did (a one-CTA plan
+// kernel: 6 us, and 13 us to check 4096 block ids).  Block ids are checked by
+// the pieces that attend to them: each item of a sequence covers all its keys,
+// so a bad id is met by every row's item, and a piece that meets one poisons
+// its item (l = -1).
 #pragma once
 
 #include <cstddef>
 #include <cstdint>
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "pa_internal.h"
@@ -35,83 +43,295 @@ struct CrossArgs {
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* query_start;
-  int num_seqs, num_rows, num_q_heads, num_kv_heads, head_dim;
+  int num_seqs, num_rows, num_q_heads, num_kv_heads;
   int group_log2;              // log2 of the query heads per KV head
   int max_blocks_per_seq, num_blocks, len_cap;
   float scale_log2;            // scale * log2(e)
   int32_t* err_flag;
-  // the cut of the work
-  int cols, keys;              // columns of an item, keys of a tile
-  int max_workers;             // workers of the launch
-  int min_tiles;               // a worker's share is at least this long
   // workspace
-  long long* head;             // {tiles, workers}
-  int4* rec;                   // [max_workers]: {sequence, item, tile, tiles of the share}
-  int4* meta;                  // [num_seqs]: {first row, rows, keys, groups of columns}
-  long long* start;            // [num_seqs + 1]: tiles before each sequence
-  float2* part_ml;             // [2 max_workers][cols]: running max (log2 units), sum of weights
-  float* part_o;               // [2 max_workers][cols][head_dim]
-  CUtensorMap tm_k;            // caches as [num_blocks * Hkv * 16][head_dim] (tensor loads)
+  unsigned* count;             // [workers][column tiles]: partials stored of the item that begins
+                               // in the worker and goes on; zero between calls
+  float2* part_ml;             // [slots][columns]: running max (log2 units), sum of weights (< 0: poisoned)
+  float* part_o;               // [slots][column tiles][D / 8][columns of a tile][8]
+  CUtensorMap tm_k;            // bf16: caches as [num_blocks * Hkv * 16][D], boxes 16 x 64, SW128
   CUtensorMap tm_v;
 };
 
-// How the work of a call is cut, and by which kernel it is done.
-struct CrossPlan {
-  int cols, keys, max_workers, min_tiles;
-  size_t rec_off, meta_off, start_off, ml_off, o_off, bytes;
+// A kernel and how it cuts the work.
+struct CrossKernel {
+  const void* fn;              // __global__ void fn(CrossArgs)
+  int threads, ctas_per_sm;
+  size_t smem;                 // dynamic shared memory of a CTA
+  int cols, keys;              // columns of an item, keys of a tile
 };
-CrossPlan cross_plan(int num_seqs, int num_rows, int num_q_heads, int num_kv_heads, int head_dim,
-                     int elem_bytes, int num_sms);
-cudaError_t launch_cross_attention(CrossArgs& a, int elem_bytes, int num_sms, cudaStream_t stream);
+// The kernel for a call (host-known sizes only).
+CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes);
+CrossKernel cross_simt_kernel_info(int head_dim);  // fp32, CUDA cores (cross_simt.cu)
+CrossKernel cross_tc_kernel_info(int head_dim);    // bf16, tcgen05 (cross_tc.cu)
+
+// Workspace: the counters first, in a place that no call's sizes change.
+constexpr size_t kCrossCountBytes = 16384;
+struct CrossLayout {
+  size_t ml_off, o_off, bytes;
+};
+CrossLayout cross_layout(const CrossKernel& k, int head_dim, int num_sms);
+cudaError_t launch_cross_attention(CrossArgs& a, const CrossKernel& k, int num_sms, cudaStream_t stream);
 
 #ifdef __CUDACC__
+__device__ __forceinline__ int cross_tiles(int n, int keys) { return n > 0 ? (n + keys - 1) / keys : 1; }
+
+// Sequence s's {first row, rows, keys, groups of `cols` columns}, checked: one
+// whose rows are out of order has none, one whose length is bad has no keys.
+__device__ __forceinline__ int4 cross_seq(const CrossArgs& a, int s, int cols, int* bit) {
+  const int r0 = __ldg(a.query_start + s), r1 = __ldg(a.query_start + s + 1);
+  int n = __ldg(a.context_lens + s);
+  *bit = 0;
+  if (!(0 <= r0 && r0 <= r1 && r1 <= a.num_rows)) {
+    *bit = kErrQuery;
+    return make_int4(0, 0, 0, 0);
+  }
+  if (r1 > r0 && (n < 0 || n > a.len_cap)) {
+    *bit = kErrContextLen;
+    n = 0;
+  }
+  // (rows * query heads fit in 31 bits)
+  return make_int4(r0, r1 - r0, n, (((r1 - r0) << a.group_log2) + cols - 1) / cols);
+}
+
+// A worker's share: `left` tiles from tile `tile` of item `item` of sequence s
+// on; the first is tile `at` of all.
+struct CrossShare {
+  long long at;
+  int left, s, item, tile;
+};
+// (in shared memory: what the end of a piece needs)
+struct CrossTotal {
+  long long W;       // tiles of the call
+  int workers;       // workers that have some
+  unsigned old[2];   // partials stored before this one, per column tile
+  long long scratch[40];
+};
+
+// Lays the work out; every thread of the CTA takes part.
+template <int THREADS>
+__device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, int keys, CrossTotal* total) {
+  long long* const scratch = total->scratch;
+  constexpr int WARPS = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, S = a.num_seqs;
+  const int per = (S + THREADS - 1) / THREADS;
+  const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
+  auto tiles_of = [&](const int4& m) -> long long {
+    return static_cast<long long>(a.num_kv_heads) * m.w * cross_tiles(m.z, keys);
+  };
+  long long local = 0;
+  int bits = 0;
+  for (int s = s0; s < s1; ++s) {
+    int bit;
+    local += tiles_of(cross_seq(a, s, cols, &bit));
+    bits |= bit;
+  }
+  if (bits && blockIdx.x == 0 && a.err_flag) atomicOr(a.err_flag, bits);
+  long long incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long t = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += t;
+  }
+  if (lane == 31) scratch[tid >> 5] = incl;
+  __syncthreads();
+  CrossShare x;
+  long long run = incl - local, W = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) {
+    if (i < (tid >> 5)) run += scratch[i];
+    W += scratch[i];
+  }
+  const int w = blockIdx.x;
+  const int workers = static_cast<int>(max(1LL, min(static_cast<long long>(gridDim.x), W)));
+  x.at = w * W / workers;
+  x.left = w < workers ? static_cast<int>((w + 1) * W / workers - x.at) : 0;
+  if (tid == 0) {
+    total->W = W;
+    total->workers = workers;
+  }
+  int* const res = reinterpret_cast<int*>(scratch + WARPS);
+  if (run <= x.at && x.at < run + local) {  // (one thread's sequences hold the first tile)
+    long long off = x.at - run;
+    for (int s = s0; s < s1; ++s) {
+      int bit;
+      const int4 m = cross_seq(a, s, cols, &bit);
+      const long long t = tiles_of(m);
+      if (off < t) {
+        const int nt = cross_tiles(m.z, keys), item = static_cast<int>(off / nt);
+        res[0] = s;
+        res[1] = item;
+        res[2] = static_cast<int>(off - static_cast<long long>(item) * nt);
+        break;
+      }
+      off -= t;
+    }
+  }
+  __syncthreads();
+  x.s = res[0];
+  x.item = res[1];
+  x.tile = res[2];
+  return x;
+}
+
 // A run of one item's tiles.
 struct CrossPiece {
   int s, kvh, grp;   // sequence, KV head, group of columns
   int t0, t1, nt;    // tiles [t0, t1) of the item's nt
-  int q0, Q, n;      // first query row, rows, keys
+  int n, live;       // keys, live columns of the group
+  long long base;    // column 0 of the group in q and out, in rows of D elements
   int slot;          // partial slot, or -1: the whole item
+  long long begin;   // the item's first tile
 };
 
-__device__ __forceinline__ int cross_tiles(int n, int keys) { return n > 0 ? (n + keys - 1) / keys : 1; }
-
-// The pieces of worker w's share, in order.
+// The pieces of a share, in order.
 struct CrossWalk {
-  int s, item, tile, left, w;
+  CrossShare x;
   int4 m;
-  __device__ __forceinline__ CrossWalk(const CrossArgs& a, int worker) : w(worker) {
-    // (written by the plan kernel while this grid may already have been
-    // launched: read through L2, never through the read-only path)
-    const int4 r = __ldcg(a.rec + worker);
-    s = r.x;
-    item = r.y;
-    tile = r.z;
-    left = worker < __ldcg(a.head + 1) ? r.w : 0;
-    m = left > 0 ? __ldcg(a.meta + s) : make_int4(0, 0, 0, 0);
+  __device__ __forceinline__ CrossWalk(const CrossArgs& a, const CrossShare& share, int cols) : x(share) {
+    int bit;
+    m = x.left > 0 ? cross_seq(a, x.s, cols, &bit) : make_int4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ bool next(const CrossArgs& a, CrossPiece* p) {
-    if (left <= 0) return false;
-    while (item >= a.num_kv_heads * m.w) {
-      if (++s >= a.num_seqs) return false;
-      m = __ldcg(a.meta + s);
-      item = tile = 0;
+  __device__ __forceinline__ bool next(const CrossArgs& a, int cols, int keys, CrossPiece* p) {
+    if (x.left <= 0) return false;
+    while (x.item >= a.num_kv_heads * m.w) {
+      if (++x.s >= a.num_seqs) return false;
+      int bit;
+      m = cross_seq(a, x.s, cols, &bit);
+      x.item = x.tile = 0;
     }
-    p->s = s;
-    p->kvh = item / m.w;
-    p->grp = item - p->kvh * m.w;
-    p->q0 = m.x;
-    p->Q = m.y;
+    p->s = x.s;
+    p->kvh = x.item / m.w;
+    p->grp = x.item - p->kvh * m.w;
     p->n = m.z;
-    p->nt = cross_tiles(m.z, a.keys);
-    p->t0 = tile;
-    p->t1 = min(p->nt, tile + left);
-    p->slot = tile > 0 ? 2 * w : p->t1 < p->nt ? 2 * w + 1 : -1;
-    left -= p->t1 - p->t0;
-    ++item;
-    tile = 0;
+    const int c0 = p->grp * cols;
+    p->live = min(cols, (m.y << a.group_log2) - c0);
+    p->base = static_cast<long long>(m.x + (c0 >> a.group_log2)) * a.num_q_heads + (p->kvh << a.group_log2);
+    p->nt = cross_tiles(m.z, keys);
+    p->t0 = x.tile;
+    p->t1 = min(p->nt, x.tile + x.left);
+    p->slot = x.tile > 0 ? 2 * blockIdx.x : p->t1 < p->nt ? 2 * blockIdx.x + 1 : -1;
+    p->begin = x.at - x.tile;
+    x.at += p->t1 - p->t0;
+    x.left -= p->t1 - p->t0;
+    ++x.item;
+    x.tile = 0;
     return true;
   }
 };
+// the workers that hold the pieces of p's item: the first, and how many
+__device__ __forceinline__ void cross_chain(const CrossTotal& t, const CrossPiece& p, int* first, int* pieces) {
+  *first = static_cast<int>(((p.begin + 1) * t.workers - 1) / t.W);
+  *pieces = static_cast<int>(((p.begin + p.nt) * t.workers - 1) / t.W) - *first + 1;
+}
+
+// column c of a piece's group in q and out, in rows of D elements past the
+// piece's base (the group begins at a query row's first head)
+__device__ __forceinline__ int cross_column(const CrossArgs& a, int c) {
+  return (c >> a.group_log2) * (a.num_q_heads - (1 << a.group_log2)) + c;
+}
+
+// Does a block that the piece attends to lie outside the cache?  Thread i of
+// `threads` looks at every threads-th id.
+__device__ __forceinline__ bool cross_bad_block(const CrossArgs& a, const CrossPiece& p, int keys, int i, int threads) {
+  const int32_t* const row = a.block_tables + static_cast<size_t>(p.s) * a.max_blocks_per_seq;
+  const int b1 = (min(p.n, p.t1 * keys) + kBlockSize - 1) / kBlockSize;
+  bool bad = false;
+  for (int b = p.t0 * (keys / kBlockSize) + i; b < b1; b += threads) {
+    const int id = __ldg(row + b);
+    bad |= !(id >= 0 && id < a.num_blocks);
+  }
+  return bad;
+}
+
+__device__ __forceinline__ void cross_store8(float* dst, const float (&x)[8]) {
+  reinterpret_cast<float4*>(dst)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(dst)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void cross_store8(__nv_bfloat16* dst, const float (&x)[8]) {
+  __nv_bfloat162 b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+  *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(b);
+}
+
+// The merge of an item's column tile t (of TILES, COLS columns each) by
+// `team` threads, once all its partials are stored and visible.  A thread
+// takes 8 dims of a column at a time, UNITS of them and AHEAD pieces in flight.
+template <typename T, int D, int COLS, int TILES, int UNITS>
+__device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece& p, int first, int pieces, int t,
+                                            int i0, int team) {
+  constexpr int AHEAD = 2;
+  const int live = min(COLS, p.live - t * COLS);
+  const int units = live * (D / 8);
+  for (int u0 = i0; u0 < units; u0 += UNITS * team) {
+    int c[UNITS], ch[UNITS];
+    float M[UNITS], L[UNITS], acc[UNITS][8];
+    bool bad[UNITS];
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      const int x = min(u0 + u * team, units - 1);  // (a repeat is stored twice, alike)
+      ch[u] = x / live;
+      c[u] = x - ch[u] * live;
+      M[u] = -INFINITY;
+      L[u] = 0.f;
+      bad[u] = false;
+#pragma unroll
+      for (int d = 0; d < 8; ++d) acc[u][d] = 0.f;
+    }
+    for (int j0 = 0; j0 < pieces; j0 += AHEAD) {
+      float2 ml[AHEAD][UNITS];
+      float4 o[AHEAD][UNITS][2];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (j0 + j >= pieces) break;
+        const int slot = j0 + j == 0 ? 2 * first + 1 : 2 * (first + j0 + j);
+        const size_t pt = static_cast<size_t>(slot) * TILES + t;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          ml[j][u] = __ldcg(a.part_ml + pt * COLS + c[u]);
+          const float4* src = reinterpret_cast<const float4*>(a.part_o + pt * COLS * D + (ch[u] * COLS + c[u]) * 8);
+          o[j][u][0] = __ldcg(src);
+          o[j][u][1] = __ldcg(src + 1);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) {
+        float mn = M[u];
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j)
+          if (j0 + j < pieces) mn = fmaxf(mn, ml[j][u].x);
+        const float sc = M[u] == -INFINITY ? 1.f : exp2f(M[u] - mn);  // (only -inf so far: zeros, or NaN)
+        L[u] *= sc;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) acc[u][d] *= sc;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+          if (j0 + j >= pieces) break;
+          bad[u] |= ml[j][u].y < 0.f;
+          const float w = ml[j][u].x == -INFINITY ? 1.f : exp2f(ml[j][u].x - mn);
+          L[u] = fmaf(w, ml[j][u].y, L[u]);
+          const float v[8] = {o[j][u][0].x, o[j][u][0].y, o[j][u][0].z, o[j][u][0].w,
+                              o[j][u][1].x, o[j][u][1].y, o[j][u][1].z, o[j][u][1].w};
+#pragma unroll
+          for (int d = 0; d < 8; ++d) acc[u][d] = fmaf(w, v[d], acc[u][d]);
+        }
+        M[u] = mn;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      const float inv = 1.f / L[u];
+#pragma unroll
+      for (int d = 0; d < 8; ++d) acc[u][d] = bad[u] ? 0.f : acc[u][d] * inv;
+      cross_store8(static_cast<T*>(a.out) + (p.base + cross_column(a, t * COLS + c[u])) * D + ch[u] * 8, acc[u]);
+    }
+  }
+}
 #endif
 
 }  // namespace pa

@@ -16,7 +16,6 @@
 #include <cuda_runtime.h>
 
 #include "cross_attention.h"
-#include "cross_kernels.h"
 #include "ptx.cuh"
 
 namespace pa {
@@ -35,27 +34,10 @@ __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0
 __device__ __forceinline__ float2 lo2(const float4& x) { return make_float2(x.x, x.y); }
 __device__ __forceinline__ float2 hi2(const float4& x) { return make_float2(x.z, x.w); }
 
-// 16 bytes of a row of T into shared memory as fp32 (zeros where !live)
-template <typename T>
-__device__ __forceinline__ void fetch(float* dst, int chunk, int swz, const T* row, bool live) {
-  if constexpr (sizeof(T) == 4) {
-    cp_async16(smem_addr(dst + 4 * (chunk ^ swz)), row + 4 * chunk, live);
-  } else {
-    uint4 r = make_uint4(0, 0, 0, 0);
-    if (live) r = *reinterpret_cast<const uint4*>(row + 8 * chunk);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float4*>(dst + 4 * ((2 * chunk + i) ^ swz)) =
-          make_float4(__uint_as_float(w[2 * i] << 16), __uint_as_float(w[2 * i] & 0xffff0000u),
-                      __uint_as_float(w[2 * i + 1] << 16), __uint_as_float(w[2 * i + 1] & 0xffff0000u));
-  }
-}
-
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
 cross_simt_kernel(const __grid_constant__ CrossArgs a) {
-  constexpr int CPR = D * sizeof(T) / 16;  // 16-byte chunks of a row
+  constexpr int CPR = D / 4;  // 16-byte chunks of a row
   constexpr int DJ = D / 64;
   extern __shared__ __align__(16) float smem[];
   float* const sQ = smem;                  // [kCols][D], 16-byte chunk c of row r at c ^ (r / 8 % 8)
@@ -65,30 +47,20 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int cg = tid >> 4, kg = tid & 15;
   float* const myP = sP + (tid >> 5) * (kKeys * 16) + ((lane >> 4) * 8);
-  const int gmask = (1 << a.group_log2) - 1;
+  __shared__ CrossTotal s_total;
 
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  CrossWalk walk(a, blockIdx.x);
+  CrossWalk walk(a, cross_share<kThreads>(a, kCols, kKeys, &s_total), kCols);
   CrossPiece p;
-  while (walk.next(a, &p)) {
-    const int c0 = p.grp * kCols;
-    // (row << group_log2 | head) of a column; -1 past the last
-    auto row_of = [&](int c) -> int {
-      const int r = (c0 + c) >> a.group_log2;
-      return r < p.Q ? p.q0 + r : -1;
-    };
-    auto head_of = [&](int c) -> int { return (p.kvh << a.group_log2) + ((c0 + c) & gmask); };
+  while (walk.next(a, kCols, kKeys, &p)) {
     if (p.n == 0) {
       for (int c = tid / 16; c < kCols; c += kThreads / 16) {
-        const int r = row_of(c);
-        if (r < 0) continue;
-        uint4* dst = reinterpret_cast<uint4*>(
-            static_cast<T*>(a.out) + (static_cast<size_t>(r) * a.num_q_heads + head_of(c)) * D);
-        for (int i = tid & 15; i < CPR; i += 16) dst[i] = make_uint4(0, 0, 0, 0);
+        if (c >= p.live) break;
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + (p.base + cross_column(a, c)) * D);
+        for (int i = tid & 15; i < CPR; i += 16) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
       continue;
     }
+    const bool bad_block = cross_bad_block(a, p, kKeys, tid, kThreads);
     const int32_t* const table = a.block_tables + static_cast<size_t>(p.s) * a.max_blocks_per_seq;
     auto load = [&](float* dst, const void* cache, int t, bool swizzle) {
       for (int i = tid; i < kKeys * CPR; i += kThreads) {
@@ -96,19 +68,19 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
         const int key = t * kKeys + r;
         const bool live = key < p.n;
         int id = live ? __ldg(table + key / kBlockSize) : 0;
-        if (id < 0 || id >= a.num_blocks) id = 0;  // (checked by the plan; never out of bounds)
-        const T* row = static_cast<const T*>(cache) +
+        if (id < 0 || id >= a.num_blocks) id = 0;  // (the piece is poisoned)
+        const float* row = static_cast<const float*>(cache) +
                        ((static_cast<size_t>(id) * a.num_kv_heads + p.kvh) * kBlockSize + key % kBlockSize) * D;
-        fetch<T>(dst + r * D, c, swizzle ? r & 7 : 0, row, live);
+        cp_async16(smem_addr(dst + r * D + 4 * (c ^ (swizzle ? r & 7 : 0))), row + 4 * c, live);
       }
       cp_commit();
     };
     __syncthreads();  // (the last piece's Q, K and V have been read)
     for (int i = tid; i < kCols * CPR; i += kThreads) {
-      const int c = i / CPR, r = row_of(c);
-      const T* row = static_cast<const T*>(a.q) +
-                     (static_cast<size_t>(max(r, 0)) * a.num_q_heads + head_of(c)) * D;
-      fetch<T>(sQ + c * D, i % CPR, (c >> 3) & 7, row, r >= 0);
+      const int c = i / CPR, k = i % CPR;
+      const long long x = p.base + cross_column(a, min(c, p.live - 1));
+      cp_async16(smem_addr(sQ + c * D + 4 * (k ^ ((c >> 3) & 7))), static_cast<const float*>(a.q) + x * D + 4 * k,
+                 c < p.live);
     }
     load(sK, a.k_cache, p.t0, true);
     load(sV, a.v_cache, p.t0, false);
@@ -212,58 +184,61 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
       if (t + 1 < p.t1) load(sV, a.v_cache, t + 1, false); else cp_commit();
     }
 
+    const bool bad = __syncthreads_or(bad_block);
+    if (bad && tid == 0 && a.err_flag) atomicOr(a.err_flag, kErrBlockId);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
       for (int off = 8; off; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
-      const int c = cg * 8 + i, r = row_of(c);
-      if (r < 0) continue;
-      if (p.slot < 0) {
-        const float inv = 1.f / l[i];
-        T* dst = static_cast<T*>(a.out) + (static_cast<size_t>(r) * a.num_q_heads + head_of(c)) * D + 4 * kg;
+      const int c = cg * 8 + i;
+      if (c >= p.live) continue;
+      const long long x = p.base + cross_column(a, c);
+      const float inv = p.slot < 0 ? 1.f / l[i] : 1.f;
 #pragma unroll
-        for (int j = 0; j < DJ; ++j) {
-          const float4 v = make_float4(o[i][2 * j].x * inv, o[i][2 * j].y * inv, o[i][2 * j + 1].x * inv,
-                                       o[i][2 * j + 1].y * inv);
-          if constexpr (sizeof(T) == 4) {
-            *reinterpret_cast<float4*>(dst + 64 * j) = v;
-          } else {
-            __nv_bfloat162 b[2] = {__floats2bfloat162_rn(v.x, v.y), __floats2bfloat162_rn(v.z, v.w)};
-            *reinterpret_cast<uint2*>(dst + 64 * j) = *reinterpret_cast<const uint2*>(b);
-          }
-        }
-      } else {
-        const size_t at = static_cast<size_t>(p.slot) * kCols + c;
-#pragma unroll
-        for (int j = 0; j < DJ; ++j)
-          *reinterpret_cast<float4*>(a.part_o + at * D + 4 * kg + 64 * j) =
-              make_float4(o[i][2 * j].x, o[i][2 * j].y, o[i][2 * j + 1].x, o[i][2 * j + 1].y);
-        if (kg == 0) a.part_ml[at] = make_float2(m[i], l[i]);
+      for (int j = 0; j < DJ; ++j) {
+        const float4 v = bad ? make_float4(0.f, 0.f, 0.f, 0.f)
+                             : make_float4(o[i][2 * j].x * inv, o[i][2 * j].y * inv, o[i][2 * j + 1].x * inv,
+                                           o[i][2 * j + 1].y * inv);
+        const int d = 4 * kg + 64 * j;
+        if (p.slot < 0)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + x * D + d) = v;
+        else
+          *reinterpret_cast<float4*>(a.part_o + static_cast<size_t>(p.slot) * kCols * D + (d / 8 * kCols + c) * 8 +
+                                     d % 8) = v;
+      }
+      if (p.slot >= 0 && kg == 0)
+        a.part_ml[static_cast<size_t>(p.slot) * kCols + c] = make_float2(m[i], bad ? -1.f : l[i]);
+    }
+    if (p.slot >= 0) {
+      int first, pieces;
+      cross_chain(s_total, p, &first, &pieces);
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_total.old[0] = atomicInc(a.count + first, pieces - 1);
+      __syncthreads();
+      if (s_total.old[0] == static_cast<unsigned>(pieces - 1)) {
+        __threadfence();
+        cross_merge<float, D, kCols, 1, 1>(a, p, first, pieces, 0, tid, kThreads);
       }
     }
   }
   cp_wait<0>();
 }
 
-template <typename T, int D>
+template <int D>
 CrossKernel info() {
   CrossKernel k{};
-  k.fn = reinterpret_cast<const void*>(&cross_simt_kernel<T, D>);
+  k.fn = reinterpret_cast<const void*>(&cross_simt_kernel<D>);
   k.threads = kThreads;
   k.ctas_per_sm = D == 64 ? 3 : 2;
-  k.workers_per_cta = 1;
   k.smem = (static_cast<size_t>(kCols) * D + 2 * kKeys * D + 4 * kKeys * 16) * sizeof(float);
   k.cols = kCols;
   k.keys = kKeys;
-  k.min_tiles = 1;
   return k;
 }
 
 }  // namespace
 
-CrossKernel cross_simt_kernel_info(int head_dim, int elem_bytes) {
-  if (elem_bytes == 4) return head_dim == 64 ? info<float, 64>() : info<float, 128>();
-  return head_dim == 64 ? info<__nv_bfloat16, 64>() : info<__nv_bfloat16, 128>();
-}
+CrossKernel cross_simt_kernel_info(int head_dim) { return head_dim == 64 ? info<64>() : info<128>(); }
 
 }  // namespace pa

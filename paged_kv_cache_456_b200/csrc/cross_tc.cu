@@ -16,12 +16,19 @@
 //                   lane c): its q row, S row, P row and O row;
 //   warp 8          producer: K and V tiles into one ring by 2-D tensor loads
 //                   (16-row blocks found through the block table);
-//   warps 10, 11    none (they complete the third warpgroup);
 //   warp 9          MMA issue, in the order  P_A V, S_A', P_B V, S_B'  where '
 //                   is the next tile of the worker's share, of the next piece
 //                   at a piece's end: one tile's softmax always runs beside
 //                   the other's MMAs.  P is handed over in halves of 64 keys,
-//                   so that its product starts half a softmax early.
+//                   so that its product starts half a softmax early;
+//   warps 10, 11    the q rows of tile A, of tile B, of the next piece as soon
+//                   as this piece's last scores are computed.
+// The softmax of a tile takes the last running maximum on trust: the first
+// half's weights are computed while the tile's own maximum is, and computed
+// again in the rare case that it exceeds the running one by 2^8 or more.
+// The output leaves through a staging area of the warp, so that stores (as
+// the q loads) touch whole rows: one row per lane and instruction cost 2000
+// cycles a tile in the load-store unit, and delayed what was queued behind.
 // A piece with at most 128 columns leaves tile B out.  Every mbarrier wait is
 // bounded; a wait that runs out sets PA_ERRBIT_TIMEOUT and every role leaves.
 #include <cstdint>
@@ -31,7 +38,6 @@
 #include <cuda_runtime.h>
 
 #include "cross_attention.h"
-#include "cross_kernels.h"
 #include "ptx.cuh"
 #include "tc.cuh"
 
@@ -42,9 +48,6 @@ constexpr int kCols = 128, kTiles = 2, kKeys = 128;
 constexpr int kBlocks = kKeys / kBlockSize;  // blocks of a K/V tile
 constexpr int kWg = 128;                     // threads of a softmax warpgroup
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kThreads = 384;
-// registers: 168 a thread at launch (384 x 168 = 64512), then 208 for the two
-// softmax warpgroups and 80 for the third (256 x 208 + 128 x 80 = 63488)
-constexpr int kRegsSoftmax = 208, kRegsRest = 80;
 constexpr int kTmemCols = 512;               // S_t at 128 t, O_t at 256 + 128 t
 constexpr float kGrow = 8.f;                 // log2 growth of a maximum before O is rescaled
 
@@ -54,8 +57,9 @@ struct Shape {
   static constexpr int QT = kCols * D * 2;      // bytes of a Q tile
   static constexpr int KT = kKeys * D * 2;      // bytes of a K or V tile
   static constexpr int HALF = kKeys * 128;      // bytes of a 64-element half of it
-  static constexpr int NS = D == 128 ? 5 : 8;   // ring slots
-  static constexpr int SMEM = 1024 + kTiles * QT + NS * KT + 256;
+  static constexpr int NS = D == 128 ? 4 : 8;   // ring slots
+  static constexpr int STAGE = 32 * 128;        // bytes of a softmax warp's staging area: 32 rows x 64 elements
+  static constexpr int SMEM = 1024 + kTiles * QT + NS * KT + 8 * STAGE + 256;
 };
 
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
@@ -92,33 +96,48 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ void st_wide(void* p, const uint32_t (&w)[8], bool wide) {
-  if (wide) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
-                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                 : "memory");
-  } else {
-    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-  }
-}
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool fill) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0)
                : "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-__device__ __forceinline__ int live_tiles(const CrossArgs& a, const CrossPiece& p) {
-  return (static_cast<long long>(p.Q) << a.group_log2) - static_cast<long long>(p.grp) * (kTiles * kCols) > kCols
-             ? 2 : 1;
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
 }
+
+// ---- pieces of the softmax: 32 scores of a column -----------------------------
+__device__ __forceinline__ void maxima(const uint32_t (&s)[32], float (&m)[4]) {
+#pragma unroll
+  for (int k = 0; k < 32; k += 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + i + 4]));
+  }
+}
+// 2^(s mul - m) as bf16 pairs in w[at, at + 16), added up in l before the rounding
+__device__ __forceinline__ void weights(const uint32_t (&s)[32], float mul, float m, uint32_t (&w)[32], int at,
+                                        float2 (&l)[2]) {
+  // (a column that saw only -inf: an offset of 0 keeps its weights at 0)
+  const float nm = m == -INFINITY ? 0.f : -m;
+  const float2 mul2 = make_float2(mul, mul), nm2 = make_float2(nm, nm);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const float2 x =
+        __ffma2_rn(make_float2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])), mul2, nm2);
+    const float2 y = make_float2(ex2(x.x), ex2(x.y));
+    l[e & 1] = __fadd2_rn(l[e & 1], y);
+    w[at + e] = pack_bf16(y.x, y.y);
+  }
+}
+__device__ __forceinline__ void store_p(uint32_t addr, const uint32_t (&w)[32]) {
+  tc::tmem_st32(addr, w);
+  tc::tmem_wait_st();
+}
+
+__device__ __forceinline__ int live_tiles(const CrossPiece& p) { return p.live > kCols ? 2 : 1; }
 // the next piece that has keys
 __device__ __forceinline__ bool next_keys(CrossWalk& w, const CrossArgs& a, CrossPiece* p) {
-  while (w.next(a, p))
+  while (w.next(a, kTiles * kCols, kKeys, p))
     if (p->n > 0) return true;
   return false;
 }
@@ -134,15 +153,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
   unsigned char* const sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   unsigned char* const sQ = sm;                  // [kTiles][QT]
   unsigned char* const sR = sQ + kTiles * QT;    // [NS][KT]: K and V tiles in turn
-  const uint32_t b0 = smem_addr(sR + NS * KT);
-  // barriers: full[NS] empty[NS] | per tile: sfull, p[2], odone, qfull | drain
+  unsigned char* const sO = sR + NS * KT;        // [8 warps][STAGE]
+  const uint32_t b0 = smem_addr(sO + 8 * C::STAGE);
+  // barriers: full[NS] empty[NS] | per tile: sfull, p[2], odone, qfull, qempty, sync | drain
   auto FULL = [&](int i) { return b0 + 8 * i; };
   auto EMPTY = [&](int i) { return b0 + 8 * (NS + i); };
-  auto TB = [&](int t, int i) { return b0 + 8 * (2 * NS + 5 * t + i); };
-  enum { SFULL = 0, P0 = 1, ODONE = 3, QFULL = 4 };
-  const uint32_t DRAIN = b0 + 8 * (2 * NS + 5 * kTiles);
+  auto TB = [&](int t, int i) { return b0 + 8 * (2 * NS + 7 * t + i); };
+  enum { SFULL = 0, P0 = 1, ODONE = 3, QFULL = 4, QEMPTY = 5, SYNC = 6 };
+  const uint32_t DRAIN = b0 + 8 * (2 * NS + 7 * kTiles);
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ CrossTotal s_total;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -155,7 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       mbar_init(TB(t, P0), kWg);
       mbar_init(TB(t, P0 + 1), kWg);
       mbar_init(TB(t, ODONE), 1);
-      mbar_init(TB(t, QFULL), kWg);
+      mbar_init(TB(t, QFULL), 32);
+      mbar_init(TB(t, QEMPTY), 1);
+      mbar_init(TB(t, SYNC), kWg);
     }
     mbar_init(DRAIN, 1);
     s_abort = 0;
@@ -166,21 +189,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
-  __syncthreads();
+  const CrossShare share = cross_share<kThreads>(a, kTiles * kCols, kKeys, &s_total);  // (synchronises the CTA)
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
-
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // (the plan)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   auto timeout = [&]() {
     if (atomicExch(&s_abort, 1) == 0 && a.err_flag) atomicOr(a.err_flag, kErrTimeout);
   };
   auto aborted = [&]() { return __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort) != 0); };
-  CrossWalk walk(a, blockIdx.x);
+  CrossWalk walk(a, share, kTiles * kCols);
 
-  if (warp >= 8) {
-  regs_dec<kRegsRest>();
   if (warp == kProducerWarp) {
     // ---------------- producer: K(0) V(0) K(1) V(1) ... over all steps ----------------
     const int oob = a.num_blocks * a.num_kv_heads * kBlockSize;  // a row past the caches: zeros
@@ -233,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     int pn[kTiles] = {0, 0}, qn[kTiles] = {0, 0};
     bool ok = true;
     // S_t of the step `s`, whose K has landed
-    auto issue_s = [&](int t, int s, bool last) {
+    auto issue_s = [&](int t, int s, bool last, bool q_done) {
       const int st = (2 * s) % NS;
       const uint64_t qd = tc::sdesc_advance(qdesc, t * QT), kd = tc::sdesc_advance(kdesc, st * KT);
       if (tc::elect_one()) {
@@ -244,18 +262,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         }
         tc::commit(TB(t, SFULL));
         if (last) tc::commit(EMPTY(st));
+        if (q_done) tc::commit(TB(t, QEMPTY));
       }
       __syncwarp();
     };
     CrossPiece cur, nxt;
     bool have = next_keys(walk, a, &cur);
-    int live = have ? live_tiles(a, cur) : 0, nlive = 0;
+    int live = have ? live_tiles(cur) : 0, nlive = 0;
     if (have) {
       ok = wait_all(FULL(0), 0);
       for (int t = 0; t < live && ok; ++t) {
         ok = wait_all(TB(t, QFULL), (qn[t]++) & 1);
         tc::fence_after_sync();
-        if (ok) issue_s(t, 0, t == live - 1);
+        if (ok) issue_s(t, 0, t == live - 1, cur.t0 + 1 == cur.t1);
       }
     }
     int j = cur.t0;
@@ -266,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         nlive = live;
       } else {
         have_next = next_keys(walk, a, &nxt);
-        nlive = have_next ? live_tiles(a, nxt) : 0;
+        nlive = have_next ? live_tiles(nxt) : 0;
       }
       const int vi = 2 * step + 1, ki = vi + 1;
       const uint64_t vd = tc::sdesc_advance(vdesc, (vi % NS) * KT);
@@ -298,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
           if (t == 0 && !wait_all(FULL(ki % NS), (ki / NS) & 1)) { ok = false; break; }
           if (!same && !wait_all(TB(t, QFULL), (qn[t]++) & 1)) { ok = false; break; }
           tc::fence_after_sync();
-          issue_s(t, step + 1, t == nlive - 1);
+          issue_s(t, step + 1, t == nlive - 1, same ? j + 2 == cur.t1 : nxt.t0 + 1 == nxt.t1);
         }
       }
       ++step;
@@ -316,204 +335,240 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     if (tc::elect_one()) tc::commit(DRAIN);
     wait_all(DRAIN, 0);
     __syncwarp();
-  }
+  } else if (warp > kMmaWarp) {
+    // ---------------- q rows of tile t, whole rows at a time --------------------------
+    const int t = warp - kMmaWarp - 1;
+    int qn = 0;
+    bool ok = true;
+    CrossPiece p;
+    while (next_keys(walk, a, &p)) {
+      if (t >= live_tiles(p)) continue;
+      if (aborted() || (qn > 0 && !wait_all(TB(t, QEMPTY), (qn - 1) & 1))) {
+        ok = false;
+        break;
+      }
+      ++qn;
+      const uint32_t qb = smem_addr(sQ + t * QT);
+      constexpr int CPR = D / 8;  // 16-byte chunks of a row
+      const int k = lane % CPR, c0 = lane / CPR;
+      const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(a.q) + p.base * D + k * 8;
+      const int live = p.live - t * kCols;
+#pragma unroll 8
+      for (int i = 0; i < kCols; i += 32 / CPR) {
+        const int c = c0 + i;
+        cp_async16_zfill(qb + (k / 8) * (kCols * 128) + c * 128 + (((k ^ c) & 7) << 4),
+                         src + cross_column(a, t * kCols + min(c, live - 1)) * D, c < live);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async_smem();
+      mbar_arrive(TB(t, QFULL));
+    }
+    if (!ok) timeout();
   } else {
-    regs_inc<kRegsSoftmax>();
     // ---------------- softmax: warpgroup t serves tile t, thread col its column -------
     const int t = warp / 4, col = tid % kWg;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
     const uint32_t s_addr = lane_base + t * kKeys, o_addr = lane_base + kTiles * kKeys + t * 128;
-    const bool wide_out = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
-    const bool wide_part = reinterpret_cast<uintptr_t>(a.part_o) % 32 == 0;
-    int step = 0, sn = 0, on = 0;
+    unsigned char* const stage = sO + warp * C::STAGE;
+    int step = 0, sn = 0, on = 0, syncs = 0;
     bool ok = true;
-    // this column's (row, head) in piece y as an index into q and out, -1: none
-    auto column_of = [&](const CrossPiece& y) -> long long {
-      const long long gc = static_cast<long long>(y.grp) * (kTiles * kCols) + t * kCols + col;
-      const long long r = gc >> a.group_log2;
-      if (r >= y.Q) return -1;
-      return (y.q0 + r) * a.num_q_heads + (y.kvh << a.group_log2) + (gc & ((1 << a.group_log2) - 1));
+    auto group_sync = [&]() -> bool {  // the 128 threads of this warpgroup
+      mbar_arrive(TB(t, SYNC));
+      return wait_all(TB(t, SYNC), (syncs++) & 1);
     };
-    auto load_q = [&](long long c) {
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (c >= 0 ? c : 0) * D;
-      const uint32_t qb = smem_addr(sQ + t * QT) + col * 128;
+    CrossPiece p;
+    while (ok && walk.next(a, kTiles * kCols, kKeys, &p)) {
+      const bool mine = t < live_tiles(p);
+      // rows of this warp's columns at `base`, 64 elements of each row, from
+      // the staging area (chunk i of row r at i ^ (r % 8)) or zeros
+      auto put_rows = [&](int base, bool zeros) {
+        const int i = lane % 8;
+        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.out) + p.base * D + base + 8 * i;
+        const int c0 = t * kCols + (warp % 4) * 32 + lane / 8;
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i)
-        cp_async16_zfill(qb + (i / 8) * (kCols * 128) + (((i % 8) ^ (col % 8)) << 4), src + i * 8, c >= 0);
-    };
-    auto hand_q = [&]() {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      mbar_arrive(TB(t, QFULL));
-    };
-    CrossPiece p, nxt;
-    bool have = walk.next(a, &p), q_handed = false;
-    while (have && ok) {
-      const bool have_next = walk.next(a, &nxt);
-      const bool mine = t < live_tiles(a, p);
-      const long long c = column_of(p);
+        for (int k = 0; k < 32; k += 4) {
+          const int r = k + lane / 8;
+          uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((i ^ (r & 7)) << 4));
+          if (zeros) v = make_uint4(0, 0, 0, 0);
+          if (c0 + k < p.live) *reinterpret_cast<uint4*>(dst + cross_column(a, c0 + k) * D) = v;
+        }
+      };
       if (p.n == 0) {
-        if (mine && c >= 0) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + c * D);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
-        }
-      } else if (!mine) {
-        step += p.t1 - p.t0;
-      } else {
-        // (Q of a piece that follows another with keys was handed over there)
-        if (!q_handed) {
-          load_q(c);
-          hand_q();
-        }
-        q_handed = false;
-        const bool ahead = have_next && nxt.n > 0 && t < live_tiles(a, nxt);
-        float m_run = -INFINITY;
-        float2 l2[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) l2[i] = make_float2(0.f, 0.f);
-        for (int j = p.t0; j < p.t1; ++j, ++step) {
-          if (aborted() || !wait_all(TB(t, SFULL), (sn++) & 1)) { ok = false; break; }
-          tc::fence_after_sync();
-          uint32_t sv[2][64];
-          tc::tmem_ld64(s_addr, sv[0]);
-          tc::tmem_ld64(s_addr + 64, sv[1]);
-          tc::tmem_wait_ld(sv[0]);
-          tc::tmem_wait_ld(sv[1]);
-          if (j == p.t1 - 1 && ahead) load_q(column_of(nxt));  // (its last S of this piece is complete)
-          const int kb = j * kKeys;
-          // Scores in log2 units are sv * mul: whole tiles under a positive
-          // scale keep the raw scores (the maximum commutes with the rounded
-          // product); otherwise they are scaled here, and keys past the end
-          // set to -inf.
-          float mul = a.scale_log2;
-          if (kb + kKeys > p.n || !(mul > 0.f)) {
-#pragma unroll
-            for (int k = 0; k < kKeys; ++k)
-              sv[k / 64][k % 64] =
-                  kb + k < p.n ? __float_as_uint(__uint_as_float(sv[k / 64][k % 64]) * mul) : 0xff800000u;
-            mul = 1.f;
-          }
-          float m8[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m8[i] = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < kKeys; k += 16) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              m8[i] = max3(m8[i], __uint_as_float(sv[k / 64][k % 64 + i]),
-                           __uint_as_float(sv[k / 64][k % 64 + i + 8]));
-          }
-          const float mx = fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]), max3(m8[5], m8[6], m8[7])) * mul;
-          const bool grow = mx > m_run + kGrow;
-          if (__any_sync(0xffffffffu, grow)) {
-            float al = 1.f;
-            if (grow) {
-              al = ex2(m_run - mx);  // (0 while nothing was seen)
-              m_run = mx;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) l2[i] = __fmul2_rn(l2[i], make_float2(al, al));
-            if (j > p.t0) {
-              // (S of this tile was issued behind P V of the last one: O is complete)
-#pragma unroll 1
-              for (int i = 0; i < D / 32; ++i) {
-                uint32_t r[32];
-                tc::tmem_ld32(o_addr + i * 32, r);
-                tc::tmem_wait_ld(r);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * al);
-                tc::tmem_st32(o_addr + i * 32, r);
-              }
-            }
-          }
-          // (a column that saw only -inf: an offset of 0 keeps its weights at 0)
-          const float nm = m_run == -INFINITY ? 0.f : -m_run;
-          const float2 mul2 = make_float2(mul, mul), nm2 = make_float2(nm, nm);
-          // Rows past the end in the last block hold stale data, and 0 x NaN
-          // would poison O: tile A's warpgroup clears them before its first P V
-          const int tail = p.n % kBlockSize;
-          if (t == 0 && tail && p.n - kb < kKeys) {
-            const int vi = 2 * step + 1;
-            if (!wait_all(FULL(vi % NS), (vi / NS) & 1)) { ok = false; break; }
-            unsigned char* const vt = sR + (vi % NS) * KT;
-            const int r0 = p.n - kb, nr = kBlockSize - tail;
-            for (int i = col; i < nr * 8 * KB; i += kWg) {
-              const int h = i / (nr * 8), r = r0 + (i / 8) % nr;
-              *reinterpret_cast<uint4*>(vt + h * HALF + r * 128 + ((i % 8) << 4)) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float2 x = __ffma2_rn(
-                  make_float2(__uint_as_float(sv[h][2 * e]), __uint_as_float(sv[h][2 * e + 1])), mul2, nm2);
-              const float2 y = make_float2(ex2(x.x), ex2(x.y));
-              l2[e & 3] = __fadd2_rn(l2[e & 3], y);
-              const __nv_bfloat162 pp = __float22bfloat162_rn(y);
-              w[e] = *reinterpret_cast<const uint32_t*>(&pp);
-            }
-            tc::tmem_st32(s_addr + 32 * h, w);
-            tc::tmem_wait_st();
-            tc::fence_before_sync();
-            mbar_arrive(TB(t, P0 + h));
-          }
-        }
-        if (!ok) break;
-        if (ahead) {
-          // the next piece's first S runs while this piece's O goes out
-          hand_q();
-          q_handed = true;
-        }
-        const float2 la = __fadd2_rn(__fadd2_rn(l2[0], l2[1]), __fadd2_rn(l2[2], l2[3]));
-        const float l_run = la.x + la.y;
-        if (!wait_all(TB(t, ODONE), (on++) & 1)) { ok = false; break; }
-        tc::fence_after_sync();
-        const bool whole = p.slot < 0;
-        const float inv = 1.f / l_run;
-        const size_t at = whole ? 0 : static_cast<size_t>(p.slot) * (kTiles * kCols) + t * kCols + col;
-        // (every lane runs the warp-wide TMEM loads; only live columns store)
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-          uint32_t o[64];
-          tc::tmem_ld64(o_addr + 64 * h, o);
-          tc::tmem_wait_ld(o);
-          if (c < 0) continue;
-          if (whole) {
-            uint4* const dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + c * D + 64 * h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const __nv_bfloat162 pp = __floats2bfloat162_rn(__uint_as_float(o[16 * i + 2 * e]) * inv,
-                                                                __uint_as_float(o[16 * i + 2 * e + 1]) * inv);
-                w[e] = *reinterpret_cast<const uint32_t*>(&pp);
-              }
-              st_wide(dst + 2 * i, w, wide_out);
-            }
-          } else {
-            float4* const dst = reinterpret_cast<float4*>(a.part_o + at * D + 64 * h);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = o[8 * i + e];
-              st_wide(dst + 2 * i, w, wide_part);
-            }
-          }
-        }
-        if (!whole && c >= 0) a.part_ml[at] = make_float2(m_run, l_run);
-        tc::fence_before_sync();  // (O has been read before this warpgroup's next P lets it be written)
+        if (mine)
+          for (int h = 0; h < KB; ++h) put_rows(64 * h, true);
+        continue;
       }
-      p = nxt;
-      have = have_next;
+      if (!mine) {
+        step += p.t1 - p.t0;
+        continue;
+      }
+      const bool bad = __any_sync(0xffffffffu, cross_bad_block(a, p, kKeys, lane, 32));
+      float m_run = -INFINITY;
+      float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      for (int j = p.t0; j < p.t1; ++j, ++step) {
+        if (aborted() || !wait_all(TB(t, SFULL), (sn++) & 1)) { ok = false; break; }
+        tc::fence_after_sync();
+        const int kb = j * kKeys;
+        // Scores in log2 units are s * mul under a positive scale (the maximum
+        // commutes with the rounded product); a tile with keys past the end,
+        // or another scale, has its scores scaled and masked one by one.
+        const bool scaled = kb + kKeys > p.n || !(a.scale_log2 > 0.f);
+        const float mul = scaled ? 1.f : a.scale_log2;
+        bool slow = j == p.t0 || scaled;
+        uint32_t s2[32], s3[32], w[32];
+        float2 lh[2];
+        if (!slow) {
+          // the first half's weights under the running maximum, and the
+          // tile's own maximum beside them
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          lh[0] = lh[1] = make_float2(0.f, 0.f);
+          uint32_t s0[32], s1[32];
+          tc::tmem_ld32(s_addr, s0);
+          tc::tmem_wait_ld(s0);
+          tc::tmem_ld32(s_addr + 32, s1);
+          maxima(s0, m4);
+          weights(s0, mul, m_run, w, 0, lh);
+          tc::tmem_wait_ld(s1);
+          tc::tmem_ld32(s_addr + 64, s2);
+          maxima(s1, m4);
+          weights(s1, mul, m_run, w, 16, lh);
+          tc::tmem_wait_ld(s2);
+          tc::tmem_ld32(s_addr + 96, s3);
+          maxima(s2, m4);
+          tc::tmem_wait_ld(s3);
+          maxima(s3, m4);
+          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * mul;
+          slow = __any_sync(0xffffffffu, mx > m_run + kGrow);
+        }
+        if (!slow) {
+          store_p(s_addr, w);
+          tc::fence_before_sync();
+          mbar_arrive(TB(t, P0));
+          weights(s2, mul, m_run, w, 0, lh);
+          weights(s3, mul, m_run, w, 16, lh);
+          store_p(s_addr + 32, w);
+          tc::fence_before_sync();
+          mbar_arrive(TB(t, P0 + 1));
+          l2[0] = __fadd2_rn(l2[0], lh[0]);
+          l2[1] = __fadd2_rn(l2[1], lh[1]);
+          continue;
+        }
+        // The other way: the maximum in one pass over S, the weights in a
+        // second (P of a chunk overwrites only chunks read before).
+        auto chunk = [&](int c, uint32_t (&s)[32]) {
+          tc::tmem_ld32(s_addr + 32 * c, s);
+          tc::tmem_wait_ld(s);
+          if (scaled) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              s[k] = kb + 32 * c + k < p.n ? __float_as_uint(__uint_as_float(s[k]) * a.scale_log2) : 0xff800000u;
+          }
+        };
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          chunk(c, s2);
+          maxima(s2, m4);
+        }
+        const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * mul;
+        float al = 1.f;
+        if (mx > m_run + kGrow) {
+          al = ex2(m_run - mx);  // (0 while nothing was seen)
+          m_run = mx;
+        }
+        l2[0] = __fmul2_rn(l2[0], make_float2(al, al));
+        l2[1] = __fmul2_rn(l2[1], make_float2(al, al));
+        if (j > p.t0 && __any_sync(0xffffffffu, al != 1.f)) {
+          // (S of this tile was issued behind P V of the last one: O is complete)
+#pragma unroll 1
+          for (int i = 0; i < D / 32; ++i) {
+            tc::tmem_ld32(o_addr + i * 32, s2);
+            tc::tmem_wait_ld(s2);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) s2[k] = __float_as_uint(__uint_as_float(s2[k]) * al);
+            tc::tmem_st32(o_addr + i * 32, s2);
+          }
+        }
+        // Rows past the end in the last block hold stale data, and 0 x NaN
+        // would poison O: tile A's warpgroup clears them before its first P V
+        const int tail = p.n % kBlockSize;
+        if (t == 0 && tail && p.n - kb < kKeys) {
+          const int vi = 2 * step + 1;
+          if (!wait_all(FULL(vi % NS), (vi / NS) & 1)) { ok = false; break; }
+          unsigned char* const vt = sR + (vi % NS) * KT;
+          const int r0 = p.n - kb, nr = kBlockSize - tail;
+          for (int i = col; i < nr * 8 * KB; i += kWg) {
+            const int h = i / (nr * 8), r = r0 + (i / 8) % nr;
+            *reinterpret_cast<uint4*>(vt + h * HALF + r * 128 + ((i % 8) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+          chunk(2 * h, s2);
+          weights(s2, mul, m_run, w, 0, l2);
+          chunk(2 * h + 1, s2);
+          weights(s2, mul, m_run, w, 16, l2);
+          store_p(s_addr + 32 * h, w);
+          tc::fence_before_sync();
+          mbar_arrive(TB(t, P0 + h));
+        }
+      }
+      if (!ok) break;
+      // ---- the piece's O
+      const float2 la = __fadd2_rn(l2[0], l2[1]);
+      const float l_run = la.x + la.y;
+      if (bad && lane == 0 && a.err_flag) atomicOr(a.err_flag, kErrBlockId);
+      if (!wait_all(TB(t, ODONE), (on++) & 1)) { ok = false; break; }
+      tc::fence_after_sync();
+      const size_t pt = static_cast<size_t>(max(p.slot, 0)) * kTiles + t;
+      const float inv = 1.f / l_run;
+#pragma unroll 1
+      for (int h = 0; h < KB; ++h) {
+        __syncwarp();  // (the staging area has been read)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t o[32];
+          tc::tmem_ld32(o_addr + 64 * h + 32 * q, o);
+          tc::tmem_wait_ld(o);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (p.slot < 0) {
+              uint32_t v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                v[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + i) ^ (lane & 7)) << 4)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
+            } else {
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * i + e]);
+              cross_store8(a.part_o + pt * kCols * D + ((8 * h + 4 * q + i) * kCols + col) * 8, v);
+            }
+          }
+        }
+        if (p.slot < 0) {
+          __syncwarp();
+          put_rows(64 * h, bad);
+        }
+      }
+      tc::fence_before_sync();  // (O has been read before this warpgroup's next P lets it be written)
+      if (p.slot >= 0) {
+        a.part_ml[pt * kCols + col] = make_float2(m_run, bad ? -1.f : l_run);
+        int first, pieces;
+        cross_chain(s_total, p, &first, &pieces);
+        __threadfence();
+        if (!group_sync()) { ok = false; break; }
+        if (col == 0) s_total.old[t] = atomicInc(a.count + 2 * first + t, pieces - 1);
+        if (!group_sync()) { ok = false; break; }
+        if (s_total.old[t] == static_cast<unsigned>(pieces - 1)) {
+          __threadfence();
+          cross_merge<__nv_bfloat16, D, kCols, kTiles, 4>(a, p, first, pieces, t, col, kWg);
+        }
+      }
     }
     if (!ok) timeout();
-    asm volatile("cp.async.wait_all;" ::: "memory");  // (a Q left in flight by an abort)
   }
 
   // every role is out of its loop; the MMAs have completed
@@ -529,11 +584,9 @@ CrossKernel info() {
   k.fn = reinterpret_cast<const void*>(&cross_tc_kernel<D>);
   k.threads = kThreads;
   k.ctas_per_sm = 1;
-  k.workers_per_cta = 1;
   k.smem = Shape<D>::SMEM;
   k.cols = kTiles * kCols;
   k.keys = kKeys;
-  k.min_tiles = 1;
   return k;
 }
 

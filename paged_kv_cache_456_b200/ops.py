@@ -285,15 +285,14 @@ def prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 def make_cross_attention_workspace(num_seqs: int, num_query_tokens: int, num_q_heads: int,
                                    num_kv_heads: int, head_dim: int, max_context_len: int,
                                    dtype: torch.dtype = torch.bfloat16, device="cuda") -> torch.Tensor:
-    """A workspace of the size ``pa_cross_attention`` needs for these sizes (its contents do
-    not matter)."""
+    """A zero-filled workspace of the size ``pa_cross_attention`` needs."""
     n = ctypes.c_size_t(0)
     with torch.cuda.device(device):
         _check(library().pa_cross_attention_workspace_size(
             num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim, int(max_context_len),
             PA_BF16 if dtype == torch.bfloat16 else PA_F32, ctypes.byref(n)),
             "pa_cross_attention_workspace_size")
-    return torch.empty(max(n.value, 16), dtype=torch.uint8, device=device)
+    return torch.zeros(max(n.value, 16), dtype=torch.uint8, device=device)
 
 
 def cross_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,

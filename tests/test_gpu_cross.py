@@ -68,9 +68,8 @@ class Case:
         self.max_keys = max(keys)
 
     def workspace(self):
-        ws = ops.make_cross_attention_workspace(len(self.rows), self.T, self.hkv * self.G, self.hkv, self.D, self.max_keys,
-                                                dtype=self.dt)
-        return ws.fill_(255)
+        return ops.make_cross_attention_workspace(len(self.rows), self.T, self.hkv * self.G, self.hkv, self.D, self.max_keys,
+                                                  dtype=self.dt)
 
     def call(self, out=None, ws=None, **kw):
         out = torch.full_like(self.q, 7.0) if out is None else out
