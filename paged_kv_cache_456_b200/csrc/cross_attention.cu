@@ -15,6 +15,10 @@ namespace {
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
+// bf16: up to this many query columns a (sequence, KV head), on average, go to
+// the kernel that streams K and V past them.
+constexpr int kFewColumns = 32;
+
 std::mutex g_mu;
 std::map<std::pair<int, const void*>, bool> g_ready;  // (device, kernel): its shared memory limit is set
 
@@ -22,6 +26,9 @@ std::map<std::pair<int, const void*>, bool> g_ready;  // (device, kernel): its s
 
 CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes) {
   if (elem_bytes == 4) return cross_simt_kernel_info(head_dim);
+  const long long columns =
+      num_seqs > 0 ? (static_cast<long long>(num_rows) * group + num_seqs - 1) / num_seqs : 0;
+  if (columns <= kFewColumns) return cross_few_kernel_info(head_dim, static_cast<int>(columns));
   return cross_tc_kernel_info(head_dim);
 }
 

@@ -67,7 +67,9 @@ struct CrossKernel {
 // The kernel for a call (host-known sizes only).
 CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes);
 CrossKernel cross_simt_kernel_info(int head_dim);  // fp32, CUDA cores (cross_simt.cu)
-CrossKernel cross_tc_kernel_info(int head_dim);    // bf16, tcgen05 (cross_tc.cu)
+CrossKernel cross_tc_kernel_info(int head_dim);    // bf16, many columns: tcgen05 (cross_tc.cu)
+// bf16, about `columns` (at most 32) query columns a (sequence, KV head): mma.sync (cross_few.cu)
+CrossKernel cross_few_kernel_info(int head_dim, int columns);
 
 // Workspace: the counters first, in a place that no call's sizes change.
 constexpr size_t kCrossCountBytes = 16384;
@@ -148,8 +150,15 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
   }
   const int w = blockIdx.x;
   const int workers = static_cast<int>(max(1LL, min(static_cast<long long>(gridDim.x), W)));
-  x.at = w * W / workers;
-  x.left = w < workers ? static_cast<int>((w + 1) * W / workers - x.at) : 0;
+  // (64-bit division costs hundreds of cycles: only where it is needed)
+  if (W < (1 << 20)) {
+    const unsigned u = static_cast<unsigned>(W);
+    x.at = w * u / workers;  // (at most 2^11 workers)
+    x.left = w < workers ? static_cast<int>((w + 1) * u / workers) - static_cast<int>(x.at) : 0;
+  } else {
+    x.at = w * W / workers;
+    x.left = w < workers ? static_cast<int>((w + 1) * W / workers - x.at) : 0;
+  }
   if (tid == 0) {
     total->W = W;
     total->workers = workers;
@@ -162,7 +171,8 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
       const int4 m = cross_seq(a, s, cols, &bit);
       const long long t = tiles_of(m);
       if (off < t) {
-        const int nt = cross_tiles(m.z, keys), item = static_cast<int>(off / nt);
+        const int nt = cross_tiles(m.z, keys);
+        const int item = off < (1LL << 31) ? static_cast<int>(off) / nt : static_cast<int>(off / nt);
         res[0] = s;
         res[1] = item;
         res[2] = static_cast<int>(off - static_cast<long long>(item) * nt);
@@ -225,8 +235,14 @@ struct CrossWalk {
 };
 // the workers that hold the pieces of p's item: the first, and how many
 __device__ __forceinline__ void cross_chain(const CrossTotal& t, const CrossPiece& p, int* first, int* pieces) {
-  *first = static_cast<int>(((p.begin + 1) * t.workers - 1) / t.W);
-  *pieces = static_cast<int>(((p.begin + p.nt) * t.workers - 1) / t.W) - *first + 1;
+  if (t.W < (1 << 20)) {
+    const unsigned W = static_cast<unsigned>(t.W), b = static_cast<unsigned>(p.begin);
+    *first = static_cast<int>(((b + 1) * t.workers - 1) / W);
+    *pieces = static_cast<int>(((b + p.nt) * t.workers - 1) / W) - *first + 1;
+  } else {
+    *first = static_cast<int>(((p.begin + 1) * t.workers - 1) / t.W);
+    *pieces = static_cast<int>(((p.begin + p.nt) * t.workers - 1) / t.W) - *first + 1;
+  }
 }
 
 // column c of a piece's group in q and out, in rows of D elements past the
@@ -259,33 +275,40 @@ __device__ __forceinline__ void cross_store8(__nv_bfloat16* dst, const float (&x
   *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(b);
 }
 
+__device__ __forceinline__ void cross_store4(float* dst, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void cross_store4(__nv_bfloat16* dst, const float (&x)[4]) {
+  __nv_bfloat162 b[2] = {__floats2bfloat162_rn(x[0], x[1]), __floats2bfloat162_rn(x[2], x[3])};
+  *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(b);
+}
+
 // The merge of an item's column tile t (of TILES, COLS columns each) by
 // `team` threads, once all its partials are stored and visible.  A thread
-// takes 8 dims of a column at a time, UNITS of them and AHEAD pieces in flight.
-template <typename T, int D, int COLS, int TILES, int UNITS>
+// takes 4 dims of a column at a time, UNITS of them and AHEAD pieces in flight.
+template <typename T, int D, int COLS, int TILES, int UNITS, int AHEAD>
 __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece& p, int first, int pieces, int t,
                                             int i0, int team) {
-  constexpr int AHEAD = 2;
   const int live = min(COLS, p.live - t * COLS);
-  const int units = live * (D / 8);
+  const int units = live * (D / 4);
   for (int u0 = i0; u0 < units; u0 += UNITS * team) {
     int c[UNITS], ch[UNITS];
-    float M[UNITS], L[UNITS], acc[UNITS][8];
+    float M[UNITS], L[UNITS], acc[UNITS][4];
     bool bad[UNITS];
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       const int x = min(u0 + u * team, units - 1);  // (a repeat is stored twice, alike)
-      ch[u] = x / live;
-      c[u] = x - ch[u] * live;
+      ch[u] = x / (2 * live) * 2 + (x & 1);  // (4-dim chunks, the two of a stored 8 side by side)
+      c[u] = x % (2 * live) >> 1;
       M[u] = -INFINITY;
       L[u] = 0.f;
       bad[u] = false;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) acc[u][d] = 0.f;
+      for (int d = 0; d < 4; ++d) acc[u][d] = 0.f;
     }
     for (int j0 = 0; j0 < pieces; j0 += AHEAD) {
       float2 ml[AHEAD][UNITS];
-      float4 o[AHEAD][UNITS][2];
+      float4 o[AHEAD][UNITS];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         if (j0 + j >= pieces) break;
@@ -294,9 +317,8 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
           ml[j][u] = __ldcg(a.part_ml + pt * COLS + c[u]);
-          const float4* src = reinterpret_cast<const float4*>(a.part_o + pt * COLS * D + (ch[u] * COLS + c[u]) * 8);
-          o[j][u][0] = __ldcg(src);
-          o[j][u][1] = __ldcg(src + 1);
+          o[j][u] = __ldcg(reinterpret_cast<const float4*>(
+              a.part_o + pt * COLS * D + (ch[u] / 2 * COLS + c[u]) * 8 + (ch[u] & 1) * 4));
         }
       }
 #pragma unroll
@@ -308,17 +330,17 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
         const float sc = M[u] == -INFINITY ? 1.f : exp2f(M[u] - mn);  // (only -inf so far: zeros, or NaN)
         L[u] *= sc;
 #pragma unroll
-        for (int d = 0; d < 8; ++d) acc[u][d] *= sc;
+        for (int d = 0; d < 4; ++d) acc[u][d] *= sc;
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
           if (j0 + j >= pieces) break;
           bad[u] |= ml[j][u].y < 0.f;
           const float w = ml[j][u].x == -INFINITY ? 1.f : exp2f(ml[j][u].x - mn);
           L[u] = fmaf(w, ml[j][u].y, L[u]);
-          const float v[8] = {o[j][u][0].x, o[j][u][0].y, o[j][u][0].z, o[j][u][0].w,
-                              o[j][u][1].x, o[j][u][1].y, o[j][u][1].z, o[j][u][1].w};
-#pragma unroll
-          for (int d = 0; d < 8; ++d) acc[u][d] = fmaf(w, v[d], acc[u][d]);
+          acc[u][0] = fmaf(w, o[j][u].x, acc[u][0]);
+          acc[u][1] = fmaf(w, o[j][u].y, acc[u][1]);
+          acc[u][2] = fmaf(w, o[j][u].z, acc[u][2]);
+          acc[u][3] = fmaf(w, o[j][u].w, acc[u][3]);
         }
         M[u] = mn;
       }
@@ -327,8 +349,8 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
     for (int u = 0; u < UNITS; ++u) {
       const float inv = 1.f / L[u];
 #pragma unroll
-      for (int d = 0; d < 8; ++d) acc[u][d] = bad[u] ? 0.f : acc[u][d] * inv;
-      cross_store8(static_cast<T*>(a.out) + (p.base + cross_column(a, t * COLS + c[u])) * D + ch[u] * 8, acc[u]);
+      for (int d = 0; d < 4; ++d) acc[u][d] = bad[u] ? 0.f : acc[u][d] * inv;
+      cross_store4(static_cast<T*>(a.out) + (p.base + cross_column(a, t * COLS + c[u])) * D + ch[u] * 4, acc[u]);
     }
   }
 }

@@ -35,7 +35,7 @@ __device__ __forceinline__ float2 lo2(const float4& x) { return make_float2(x.x,
 __device__ __forceinline__ float2 hi2(const float4& x) { return make_float2(x.z, x.w); }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, D == 64 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 cross_simt_kernel(const __grid_constant__ CrossArgs a) {
   constexpr int CPR = D / 4;  // 16-byte chunks of a row
   constexpr int DJ = D / 64;
@@ -218,7 +218,7 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
       __syncthreads();
       if (s_total.old[0] == static_cast<unsigned>(pieces - 1)) {
         __threadfence();
-        cross_merge<float, D, kCols, 1, 1>(a, p, first, pieces, 0, tid, kThreads);
+        cross_merge<float, D, kCols, 1, 1, 2>(a, p, first, pieces, 0, tid, kThreads);
       }
     }
   }
@@ -230,7 +230,7 @@ CrossKernel info() {
   CrossKernel k{};
   k.fn = reinterpret_cast<const void*>(&cross_simt_kernel<D>);
   k.threads = kThreads;
-  k.ctas_per_sm = D == 64 ? 3 : 2;
+  k.ctas_per_sm = 2;
   k.smem = (static_cast<size_t>(kCols) * D + 2 * kKeys * D + 4 * kKeys * 16) * sizeof(float);
   k.cols = kCols;
   k.keys = kKeys;

@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         if (!group_sync()) { ok = false; break; }
         if (s_total.old[t] == static_cast<unsigned>(pieces - 1)) {
           __threadfence();
-          cross_merge<__nv_bfloat16, D, kCols, kTiles, 4>(a, p, first, pieces, t, col, kWg);
+          cross_merge<__nv_bfloat16, D, kCols, kTiles, 4, 2>(a, p, first, pieces, t, col, kWg);
         }
       }
     }
