@@ -202,6 +202,7 @@ struct CrossPiece {
 struct CrossWalk {
   CrossShare x;
   int4 m;
+  CrossWalk() = default;
   __device__ __forceinline__ CrossWalk(const CrossArgs& a, const CrossShare& share, int cols) : x(share) {
     int bit;
     m = x.left > 0 ? cross_seq(a, x.s, cols, &bit) : make_int4(0, 0, 0, 0);
@@ -283,6 +284,16 @@ __device__ __forceinline__ void cross_store4(__nv_bfloat16* dst, const float (&x
   *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(b);
 }
 
+// column tile t of the partial of an item's i-th piece (`first`: the worker of
+// its first)
+template <int TILES>
+__device__ __forceinline__ size_t cross_tile(int first, int i, int t) {
+  return static_cast<size_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * TILES + t;
+}
+// a piece's weight under the item's maximum (a piece that saw nothing finite
+// carries zeros, or the NaN that its scores make)
+__device__ __forceinline__ float cross_weight(float m, float M) { return m == -INFINITY ? 1.f : exp2f(m - M); }
+
 // The merge of an item's column tile t (of TILES, COLS columns each) by
 // `team` threads, once all its partials are stored and visible.  A thread
 // takes 4 dims of a column at a time, UNITS of them and AHEAD pieces in flight.
@@ -298,7 +309,7 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
 #pragma unroll
     for (int u = 0; u < UNITS; ++u) {
       const int x = min(u0 + u * team, units - 1);  // (a repeat is stored twice, alike)
-      ch[u] = x / (2 * live) * 2 + (x & 1);  // (4-dim chunks, the two of a stored 8 side by side)
+      ch[u] = x / (2 * live) * 2 + (x & 1);         // (the two chunks of a stored 8 side by side)
       c[u] = x % (2 * live) >> 1;
       M[u] = -INFINITY;
       L[u] = 0.f;
@@ -307,13 +318,20 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
       for (int d = 0; d < 4; ++d) acc[u][d] = 0.f;
     }
     for (int j0 = 0; j0 < pieces; j0 += AHEAD) {
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const size_t pt = cross_tile<TILES>(first, min(j0 + j, pieces - 1), t);
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) M[u] = fmaxf(M[u], __ldcg(a.part_ml + pt * COLS + c[u]).x);
+      }
+    }
+    for (int j0 = 0; j0 < pieces; j0 += AHEAD) {
       float2 ml[AHEAD][UNITS];
       float4 o[AHEAD][UNITS];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         if (j0 + j >= pieces) break;
-        const int slot = j0 + j == 0 ? 2 * first + 1 : 2 * (first + j0 + j);
-        const size_t pt = static_cast<size_t>(slot) * TILES + t;
+        const size_t pt = cross_tile<TILES>(first, j0 + j, t);
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
           ml[j][u] = __ldcg(a.part_ml + pt * COLS + c[u]);
@@ -322,27 +340,18 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
         }
       }
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        float mn = M[u];
+      for (int j = 0; j < AHEAD; ++j) {
+        if (j0 + j >= pieces) break;
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j)
-          if (j0 + j < pieces) mn = fmaxf(mn, ml[j][u].x);
-        const float sc = M[u] == -INFINITY ? 1.f : exp2f(M[u] - mn);  // (only -inf so far: zeros, or NaN)
-        L[u] *= sc;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) acc[u][d] *= sc;
-#pragma unroll
-        for (int j = 0; j < AHEAD; ++j) {
-          if (j0 + j >= pieces) break;
+        for (int u = 0; u < UNITS; ++u) {
           bad[u] |= ml[j][u].y < 0.f;
-          const float w = ml[j][u].x == -INFINITY ? 1.f : exp2f(ml[j][u].x - mn);
+          const float w = cross_weight(ml[j][u].x, M[u]);
           L[u] = fmaf(w, ml[j][u].y, L[u]);
           acc[u][0] = fmaf(w, o[j][u].x, acc[u][0]);
           acc[u][1] = fmaf(w, o[j][u].y, acc[u][1]);
           acc[u][2] = fmaf(w, o[j][u].z, acc[u][2]);
           acc[u][3] = fmaf(w, o[j][u].w, acc[u][3]);
         }
-        M[u] = mn;
       }
     }
 #pragma unroll

@@ -32,6 +32,7 @@
 // A piece with at most 128 columns leaves tile B out.  Every mbarrier wait is
 // bounded; a wait that runs out sets PA_ERRBIT_TIMEOUT and every role leaves.
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -48,6 +49,9 @@ constexpr int kCols = 128, kTiles = 2, kKeys = 128;
 constexpr int kBlocks = kKeys / kBlockSize;  // blocks of a K/V tile
 constexpr int kWg = 128;                     // threads of a softmax warpgroup
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kThreads = 384;
+// registers: 168 a thread at launch (384 x 168 = 64512), then 192 for the two
+// softmax warpgroups and 120 for the third (256 x 192 + 128 x 120 = 64512)
+constexpr int kRegsSoftmax = 192, kRegsRest = 120;
 constexpr int kTmemCols = 512;               // S_t at 128 t, O_t at 256 + 128 t
 constexpr float kGrow = 8.f;                 // log2 growth of a maximum before O is rescaled
 
@@ -135,12 +139,40 @@ __device__ __forceinline__ void store_p(uint32_t addr, const uint32_t (&w)[32]) 
 }
 
 __device__ __forceinline__ int live_tiles(const CrossPiece& p) { return p.live > kCols ? 2 : 1; }
-// the next piece that has keys
-__device__ __forceinline__ bool next_keys(CrossWalk& w, const CrossArgs& a, CrossPiece* p) {
-  while (w.next(a, kTiles * kCols, kKeys, p))
-    if (p->n > 0) return true;
-  return false;
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A warp's walk over the share and the piece it is at live in shared memory:
+// in registers they would be held through the tile loops, which have none to
+// spare.  One lane steps; a piece's fields are read again where they are used.
+struct WarpWalk {
+  CrossWalk walk;
+  CrossPiece piece;
+  __device__ __forceinline__ bool next(const CrossArgs& a, bool with_keys) {
+    bool ok = false;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0)
+      while ((ok = walk.next(a, kTiles * kCols, kKeys, &piece)) && with_keys && piece.n == 0) {
+      }
+    ok = __any_sync(0xffffffffu, ok);
+    __syncwarp();
+    return ok;
+  }
+  __device__ __forceinline__ CrossPiece get() const {
+    CrossPiece p;
+    static_assert(sizeof(CrossPiece) % 4 == 0, "copied by words");
+    const volatile int* const src = reinterpret_cast<const volatile int*>(&piece);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(CrossPiece) / 4); ++i) reinterpret_cast<int*>(&p)[i] = src[i];
+    return p;
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_constant__ CrossArgs a) {
@@ -164,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   __shared__ CrossTotal s_total;
+  __shared__ WarpWalk s_walk[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -189,7 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
-  const CrossShare share = cross_share<kThreads>(a, kTiles * kCols, kKeys, &s_total);  // (synchronises the CTA)
+  {
+    const CrossShare share = cross_share<kThreads>(a, kTiles * kCols, kKeys, &s_total);  // (synchronises the CTA)
+    if (lane == 0) s_walk[warp].walk = CrossWalk(a, share, kTiles * kCols);
+    __syncwarp();
+  }
+  WarpWalk& walk = s_walk[warp];
   tc::fence_after_sync();
   const uint32_t tmem = s_tmem;
 
@@ -197,174 +235,181 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     if (atomicExch(&s_abort, 1) == 0 && a.err_flag) atomicOr(a.err_flag, kErrTimeout);
   };
   auto aborted = [&]() { return __any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&s_abort) != 0); };
-  CrossWalk walk(a, share, kTiles * kCols);
 
-  if (warp == kProducerWarp) {
-    // ---------------- producer: K(0) V(0) K(1) V(1) ... over all steps ----------------
-    const int oob = a.num_blocks * a.num_kv_heads * kBlockSize;  // a row past the caches: zeros
-    int idx = 0;
-    bool ok = true;
-    auto issue = [&](const CUtensorMap* map, int y) -> bool {
-      const int st = idx % NS;
-      if (idx >= NS && !wait_all(EMPTY(st), ((idx / NS) - 1) & 1)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(FULL(st), KT);
-      __syncwarp();
-      if (lane < kBlocks) {
-        const uint32_t dst = smem_addr(sR + st * KT) + lane * kBlockSize * 128;
+  if (warp >= 8) {
+    regs_dec<kRegsRest>();
+    if (warp == kProducerWarp) {
+      // ---------------- producer: K(0) V(0) K(1) V(1) ... over all steps ----------------
+      const int oob = a.num_blocks * a.num_kv_heads * kBlockSize;  // a row past the caches: zeros
+      int idx = 0;
+      bool ok = true;
+      auto issue = [&](const CUtensorMap* map, int y) -> bool {
+        const int st = idx % NS;
+        if (idx >= NS && !wait_all(EMPTY(st), ((idx / NS) - 1) & 1)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(FULL(st), KT);
+        __syncwarp();
+        if (lane < kBlocks) {
+          const uint32_t dst = smem_addr(sR + st * KT) + lane * kBlockSize * 128;
 #pragma unroll
-        for (int h = 0; h < KB; ++h) tma_load_2d(dst + h * HALF, map, h * 64, y, FULL(st));
-      }
-      ++idx;
-      return true;
-    };
-    CrossPiece p;
-    while (ok && next_keys(walk, a, &p)) {
-      const int32_t* const table = a.block_tables + static_cast<size_t>(p.s) * a.max_blocks_per_seq;
-      auto rows_of = [&](int j) -> int {  // this lane's block of tile j
-        const int b = j * kBlocks + lane;
-        int y = oob;
-        if (lane < kBlocks && j < p.t1 && b * kBlockSize < p.n) {
-          const int id = __ldg(table + b);
-          if (id >= 0 && id < a.num_blocks) y = (id * a.num_kv_heads + p.kvh) * kBlockSize;
+          for (int h = 0; h < KB; ++h) tma_load_2d(dst + h * HALF, map, h * 64, y, FULL(st));
         }
-        return y;
+        ++idx;
+        return true;
       };
-      int ynext = rows_of(p.t0);
-      for (int j = p.t0; j < p.t1; ++j) {
-        const int y = ynext;
-        ynext = rows_of(j + 1);
-        if (aborted() || !issue(&a.tm_k, y) || !issue(&a.tm_v, y)) {
+      while (ok && walk.next(a, true)) {
+        const CrossPiece p = walk.get();
+        const int32_t* const table = a.block_tables + static_cast<size_t>(p.s) * a.max_blocks_per_seq;
+        auto rows_of = [&](int j) -> int {  // this lane's block of tile j
+          const int b = j * kBlocks + lane;
+          int y = oob;
+          if (lane < kBlocks && j < p.t1 && b * kBlockSize < p.n) {
+            const int id = __ldg(table + b);
+            if (id >= 0 && id < a.num_blocks) y = (id * a.num_kv_heads + p.kvh) * kBlockSize;
+          }
+          return y;
+        };
+        int ynext = rows_of(p.t0);
+        for (int j = p.t0; j < p.t1; ++j) {
+          const int y = ynext;
+          ynext = rows_of(j + 1);
+          if (aborted() || !issue(&a.tm_k, y) || !issue(&a.tm_v, y)) {
+            ok = false;
+            break;
+          }
+        }
+      }
+      if (!ok) timeout();
+      // every load issued lands before the CTA can exit
+      for (int i = max(0, idx - NS); i < idx; ++i) wait_all(FULL(i % NS), (i / NS) & 1);
+    } else if (warp == kMmaWarp) {
+      // ---------------- MMA issue --------------------------------------------------------
+      const uint64_t qdesc = tc::sdesc_sw128(smem_addr(sQ), 16, 1024);
+      const uint64_t kdesc = tc::sdesc_sw128(smem_addr(sR), 16, 1024);
+      const uint64_t vdesc = tc::sdesc_sw128(smem_addr(sR), HALF, 1024);
+      int step = 0;                       // K of this step in ring index 2 step, V in 2 step + 1
+      int pn[kTiles] = {0, 0}, qn[kTiles] = {0, 0};
+      bool ok = true;
+      // S_t of the step `s`, whose K has landed
+      auto issue_s = [&](int t, int s, bool last, bool q_done) {
+        const int st = (2 * s) % NS;
+        const uint64_t qd = tc::sdesc_advance(qdesc, t * QT), kd = tc::sdesc_advance(kdesc, st * KT);
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t qo = (k / 4) * (kCols * 128) + (k % 4) * 32, ko = (k / 4) * HALF + (k % 4) * 32;
+            tc::mma_bf16_ss(tmem + t * kKeys, tc::sdesc_advance(qd, qo), tc::sdesc_advance(kd, ko), IDESC_S, k > 0);
+          }
+          tc::commit(TB(t, SFULL));
+          if (last) tc::commit(EMPTY(st));
+          if (q_done) tc::commit(TB(t, QEMPTY));
+        }
+        __syncwarp();
+      };
+      // (of a piece this warp needs its tiles and which column tiles live)
+      int left = 0, live = 0, nleft = 0, nlive = 0;
+      auto advance = [&]() {
+        nleft = nlive = 0;
+        if (walk.next(a, true)) {
+          const CrossPiece y = walk.get();
+          nleft = y.t1 - y.t0;
+          nlive = live_tiles(y);
+        }
+      };
+      advance();
+      bool begun = false;  // O of the piece holds a product
+      left = nleft;
+      live = nlive;
+      if (left > 0) {
+        ok = wait_all(FULL(0), 0);
+        for (int t = 0; t < live && ok; ++t) {
+          ok = wait_all(TB(t, QFULL), (qn[t]++) & 1);
+          tc::fence_after_sync();
+          if (ok) issue_s(t, 0, t == live - 1, left == 1);
+        }
+      }
+      while (left > 0 && ok) {
+        const bool same = left > 1;
+        if (same) {
+          nleft = left - 1;
+          nlive = live;
+        } else {
+          advance();
+        }
+        const int vi = 2 * step + 1, ki = vi + 1;
+        const uint64_t vd = tc::sdesc_advance(vdesc, (vi % NS) * KT);
+        if (aborted()) { ok = false; break; }
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if (t < live) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (!wait_all(TB(t, P0 + h), pn[t] & 1)) { ok = false; break; }
+              if (t == 0 && h == 0 && !wait_all(FULL(vi % NS), (vi / NS) & 1)) { ok = false; break; }
+              tc::fence_after_sync();
+              if (tc::elect_one()) {
+#pragma unroll
+                for (int k = 4 * h; k < 4 * h + 4; ++k)
+                  tc::mma_bf16_ts(tmem + kTiles * kKeys + t * 128, tmem + t * kKeys + k * 8,
+                                  tc::sdesc_advance(vd, k * 16 * 128), IDESC_O, (begun || k > 0) ? 1u : 0u);
+                if (h == 1) {
+                  if (!same) tc::commit(TB(t, ODONE));
+                  if (t == live - 1) tc::commit(EMPTY(vi % NS));
+                }
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            ++pn[t];
+          }
+          if (t < nlive) {
+            if (t == 0 && !wait_all(FULL(ki % NS), (ki / NS) & 1)) { ok = false; break; }
+            if (!same && !wait_all(TB(t, QFULL), (qn[t]++) & 1)) { ok = false; break; }
+            tc::fence_after_sync();
+            issue_s(t, step + 1, t == nlive - 1, nleft == 1);
+          }
+        }
+        ++step;
+        begun = same;
+        left = nleft;
+        live = nlive;
+      }
+      if (!ok) timeout();
+      // every MMA issued has completed before the TMEM can be freed
+      if (tc::elect_one()) tc::commit(DRAIN);
+      wait_all(DRAIN, 0);
+      __syncwarp();
+    } else {
+      // ---------------- q rows of tile t, whole rows at a time --------------------------
+      const int t = warp - kMmaWarp - 1;
+      int qn = 0;
+      bool ok = true;
+      while (walk.next(a, true)) {
+        const CrossPiece p = walk.get();
+        if (t >= live_tiles(p)) continue;
+        if (aborted() || (qn > 0 && !wait_all(TB(t, QEMPTY), (qn - 1) & 1))) {
           ok = false;
           break;
         }
-      }
-    }
-    if (!ok) timeout();
-    // every load issued lands before the CTA can exit
-    for (int i = max(0, idx - NS); i < idx; ++i) wait_all(FULL(i % NS), (i / NS) & 1);
-  } else if (warp == kMmaWarp) {
-    // ---------------- MMA issue --------------------------------------------------------
-    const uint64_t qdesc = tc::sdesc_sw128(smem_addr(sQ), 16, 1024);
-    const uint64_t kdesc = tc::sdesc_sw128(smem_addr(sR), 16, 1024);
-    const uint64_t vdesc = tc::sdesc_sw128(smem_addr(sR), HALF, 1024);
-    int step = 0;                       // K of this step in ring index 2 step, V in 2 step + 1
-    int pn[kTiles] = {0, 0}, qn[kTiles] = {0, 0};
-    bool ok = true;
-    // S_t of the step `s`, whose K has landed
-    auto issue_s = [&](int t, int s, bool last, bool q_done) {
-      const int st = (2 * s) % NS;
-      const uint64_t qd = tc::sdesc_advance(qdesc, t * QT), kd = tc::sdesc_advance(kdesc, st * KT);
-      if (tc::elect_one()) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t qo = (k / 4) * (kCols * 128) + (k % 4) * 32, ko = (k / 4) * HALF + (k % 4) * 32;
-          tc::mma_bf16_ss(tmem + t * kKeys, tc::sdesc_advance(qd, qo), tc::sdesc_advance(kd, ko), IDESC_S, k > 0);
+        ++qn;
+        const uint32_t qb = smem_addr(sQ + t * QT);
+        constexpr int CPR = D / 8;  // 16-byte chunks of a row
+        const int k = lane % CPR, c0 = lane / CPR;
+        const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(a.q) + p.base * D + k * 8;
+        const int live = p.live - t * kCols;
+#pragma unroll 4
+        for (int i = 0; i < kCols; i += 32 / CPR) {
+          const int c = c0 + i;
+          cp_async16_zfill(qb + (k / 8) * (kCols * 128) + c * 128 + (((k ^ c) & 7) << 4),
+                           src + cross_column(a, t * kCols + min(c, live - 1)) * D, c < live);
         }
-        tc::commit(TB(t, SFULL));
-        if (last) tc::commit(EMPTY(st));
-        if (q_done) tc::commit(TB(t, QEMPTY));
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(TB(t, QFULL));
       }
-      __syncwarp();
-    };
-    CrossPiece cur, nxt;
-    bool have = next_keys(walk, a, &cur);
-    int live = have ? live_tiles(cur) : 0, nlive = 0;
-    if (have) {
-      ok = wait_all(FULL(0), 0);
-      for (int t = 0; t < live && ok; ++t) {
-        ok = wait_all(TB(t, QFULL), (qn[t]++) & 1);
-        tc::fence_after_sync();
-        if (ok) issue_s(t, 0, t == live - 1, cur.t0 + 1 == cur.t1);
-      }
+      if (!ok) timeout();
     }
-    int j = cur.t0;
-    while (have && ok) {
-      const bool same = j + 1 < cur.t1;
-      bool have_next = same;
-      if (same) {
-        nlive = live;
-      } else {
-        have_next = next_keys(walk, a, &nxt);
-        nlive = have_next ? live_tiles(nxt) : 0;
-      }
-      const int vi = 2 * step + 1, ki = vi + 1;
-      const uint64_t vd = tc::sdesc_advance(vdesc, (vi % NS) * KT);
-      if (aborted()) { ok = false; break; }
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) {
-        if (t < live) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!wait_all(TB(t, P0 + h), pn[t] & 1)) { ok = false; break; }
-            if (t == 0 && h == 0 && !wait_all(FULL(vi % NS), (vi / NS) & 1)) { ok = false; break; }
-            tc::fence_after_sync();
-            if (tc::elect_one()) {
-#pragma unroll
-              for (int k = 4 * h; k < 4 * h + 4; ++k)
-                tc::mma_bf16_ts(tmem + kTiles * kKeys + t * 128, tmem + t * kKeys + k * 8,
-                                tc::sdesc_advance(vd, k * 16 * 128), IDESC_O, (j > cur.t0 || k > 0) ? 1u : 0u);
-              if (h == 1) {
-                if (!same) tc::commit(TB(t, ODONE));
-                if (t == live - 1) tc::commit(EMPTY(vi % NS));
-              }
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
-          ++pn[t];
-        }
-        if (have_next && t < nlive) {
-          if (t == 0 && !wait_all(FULL(ki % NS), (ki / NS) & 1)) { ok = false; break; }
-          if (!same && !wait_all(TB(t, QFULL), (qn[t]++) & 1)) { ok = false; break; }
-          tc::fence_after_sync();
-          issue_s(t, step + 1, t == nlive - 1, same ? j + 2 == cur.t1 : nxt.t0 + 1 == nxt.t1);
-        }
-      }
-      ++step;
-      if (same) {
-        ++j;
-      } else {
-        cur = nxt;
-        j = cur.t0;
-        live = nlive;
-        have = have_next;
-      }
-    }
-    if (!ok) timeout();
-    // every MMA issued has completed before the TMEM can be freed
-    if (tc::elect_one()) tc::commit(DRAIN);
-    wait_all(DRAIN, 0);
-    __syncwarp();
-  } else if (warp > kMmaWarp) {
-    // ---------------- q rows of tile t, whole rows at a time --------------------------
-    const int t = warp - kMmaWarp - 1;
-    int qn = 0;
-    bool ok = true;
-    CrossPiece p;
-    while (next_keys(walk, a, &p)) {
-      if (t >= live_tiles(p)) continue;
-      if (aborted() || (qn > 0 && !wait_all(TB(t, QEMPTY), (qn - 1) & 1))) {
-        ok = false;
-        break;
-      }
-      ++qn;
-      const uint32_t qb = smem_addr(sQ + t * QT);
-      constexpr int CPR = D / 8;  // 16-byte chunks of a row
-      const int k = lane % CPR, c0 = lane / CPR;
-      const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(a.q) + p.base * D + k * 8;
-      const int live = p.live - t * kCols;
-#pragma unroll 8
-      for (int i = 0; i < kCols; i += 32 / CPR) {
-        const int c = c0 + i;
-        cp_async16_zfill(qb + (k / 8) * (kCols * 128) + c * 128 + (((k ^ c) & 7) << 4),
-                         src + cross_column(a, t * kCols + min(c, live - 1)) * D, c < live);
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      fence_proxy_async_smem();
-      mbar_arrive(TB(t, QFULL));
-    }
-    if (!ok) timeout();
   } else {
+    regs_inc<kRegsSoftmax>();
     // ---------------- softmax: warpgroup t serves tile t, thread col its column -------
     const int t = warp / 4, col = tid % kWg;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
@@ -376,188 +421,246 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       mbar_arrive(TB(t, SYNC));
       return wait_all(TB(t, SYNC), (syncs++) & 1);
     };
-    CrossPiece p;
-    while (ok && walk.next(a, kTiles * kCols, kKeys, &p)) {
-      const bool mine = t < live_tiles(p);
+    // Scores in log2 units are s * mul: under a positive scale the maximum commutes
+    // with the rounded product; another scale is applied to the scores one by one.
+    const float mul = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;
+    while (ok && walk.next(a, false)) {
       // rows of this warp's columns at `base`, 64 elements of each row, from
       // the staging area (chunk i of row r at i ^ (r % 8)) or zeros
-      auto put_rows = [&](int base, bool zeros) {
+      auto put_rows = [&](const CrossPiece& p, int base, bool zeros) {
         const int i = lane % 8;
         __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.out) + p.base * D + base + 8 * i;
         const int c0 = t * kCols + (warp % 4) * 32 + lane / 8;
+        uint4 v[8];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const int r = k + lane / 8;
-          uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((i ^ (r & 7)) << 4));
-          if (zeros) v = make_uint4(0, 0, 0, 0);
-          if (c0 + k < p.live) *reinterpret_cast<uint4*>(dst + cross_column(a, c0 + k) * D) = v;
+        for (int k = 0; k < 8; ++k) {
+          const int r = 4 * k + lane / 8;
+          v[k] = *reinterpret_cast<const uint4*>(stage + r * 128 + ((i ^ (r & 7)) << 4));
+          if (zeros) v[k] = make_uint4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c0 + 4 * k < p.live) *reinterpret_cast<uint4*>(dst + cross_column(a, c0 + 4 * k) * D) = v[k];
       };
-      if (p.n == 0) {
-        if (mine)
-          for (int h = 0; h < KB; ++h) put_rows(64 * h, true);
-        continue;
+      int left, tiles;  // keys from this tile on, tiles to go
+      bool bad;
+      {
+        const CrossPiece p = walk.get();
+        const bool mine = t < live_tiles(p);
+        if (p.n == 0) {
+          if (mine)
+            for (int h = 0; h < KB; ++h) put_rows(p, 64 * h, true);
+          continue;
+        }
+        tiles = p.t1 - p.t0;
+        left = p.n - p.t0 * kKeys;
+        if (!mine) {
+          step += tiles;
+          continue;
+        }
+        bad = __any_sync(0xffffffffu, cross_bad_block(a, p, kKeys, lane, 32));
       }
-      if (!mine) {
-        step += p.t1 - p.t0;
-        continue;
-      }
-      const bool bad = __any_sync(0xffffffffu, cross_bad_block(a, p, kKeys, lane, 32));
       float m_run = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      for (int j = p.t0; j < p.t1; ++j, ++step) {
+      bool begun = false;
+      for (; tiles > 0; --tiles, left -= kKeys, ++step, begun = true) {
         if (aborted() || !wait_all(TB(t, SFULL), (sn++) & 1)) { ok = false; break; }
         tc::fence_after_sync();
-        const int kb = j * kKeys;
-        // Scores in log2 units are s * mul under a positive scale (the maximum
-        // commutes with the rounded product); a tile with keys past the end,
-        // or another scale, has its scores scaled and masked one by one.
-        const bool scaled = kb + kKeys > p.n || !(a.scale_log2 > 0.f);
-        const float mul = scaled ? 1.f : a.scale_log2;
-        bool slow = j == p.t0 || scaled;
+        const bool plain = left >= kKeys && a.scale_log2 > 0.f;
+        // 32 scores of another tile made ready to be scaled by mul (keys past the end: -inf)
+        auto prepare = [&](uint32_t (&x)[32], int c) {
+          const float f = a.scale_log2 > 0.f ? 1.f : a.scale_log2;
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            x[k] = 32 * c + k < left ? __float_as_uint(__uint_as_float(x[k]) * f) : 0xff800000u;
+        };
         uint32_t s2[32], s3[32], w[32];
-        float2 lh[2];
-        if (!slow) {
-          // the first half's weights under the running maximum, and the
-          // tile's own maximum beside them
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          lh[0] = lh[1] = make_float2(0.f, 0.f);
+        float2 lh[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        // The first half's weights under the running maximum (in a piece's first
+        // tile there is none yet: they are computed again below), and the
+        // tile's own maximum beside them; the second half's scores stay.
+        auto front = [&](auto plain_tag) {
+          constexpr bool PLAIN = decltype(plain_tag)::value;
           uint32_t s0[32], s1[32];
           tc::tmem_ld32(s_addr, s0);
           tc::tmem_wait_ld(s0);
           tc::tmem_ld32(s_addr + 32, s1);
+          if (!PLAIN) prepare(s0, 0);
           maxima(s0, m4);
           weights(s0, mul, m_run, w, 0, lh);
           tc::tmem_wait_ld(s1);
           tc::tmem_ld32(s_addr + 64, s2);
+          if (!PLAIN) prepare(s1, 1);
           maxima(s1, m4);
           weights(s1, mul, m_run, w, 16, lh);
           tc::tmem_wait_ld(s2);
           tc::tmem_ld32(s_addr + 96, s3);
+          if (!PLAIN) prepare(s2, 2);
           maxima(s2, m4);
           tc::tmem_wait_ld(s3);
+          if (!PLAIN) prepare(s3, 3);
           maxima(s3, m4);
-          const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * mul;
-          slow = __any_sync(0xffffffffu, mx > m_run + kGrow);
-        }
-        if (!slow) {
-          store_p(s_addr, w);
-          tc::fence_before_sync();
-          mbar_arrive(TB(t, P0));
-          weights(s2, mul, m_run, w, 0, lh);
-          weights(s3, mul, m_run, w, 16, lh);
-          store_p(s_addr + 32, w);
-          tc::fence_before_sync();
-          mbar_arrive(TB(t, P0 + 1));
-          l2[0] = __fadd2_rn(l2[0], lh[0]);
-          l2[1] = __fadd2_rn(l2[1], lh[1]);
-          continue;
-        }
-        // The other way: the maximum in one pass over S, the weights in a
-        // second (P of a chunk overwrites only chunks read before).
-        auto chunk = [&](int c, uint32_t (&s)[32]) {
-          tc::tmem_ld32(s_addr + 32 * c, s);
-          tc::tmem_wait_ld(s);
-          if (scaled) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              s[k] = kb + 32 * c + k < p.n ? __float_as_uint(__uint_as_float(s[k]) * a.scale_log2) : 0xff800000u;
-          }
         };
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          chunk(c, s2);
-          maxima(s2, m4);
-        }
+        if (plain) front(std::true_type{}); else front(std::false_type{});
         const float mx = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]) * mul;
-        float al = 1.f;
-        if (mx > m_run + kGrow) {
-          al = ex2(m_run - mx);  // (0 while nothing was seen)
-          m_run = mx;
-        }
-        l2[0] = __fmul2_rn(l2[0], make_float2(al, al));
-        l2[1] = __fmul2_rn(l2[1], make_float2(al, al));
-        if (j > p.t0 && __any_sync(0xffffffffu, al != 1.f)) {
-          // (S of this tile was issued behind P V of the last one: O is complete)
-#pragma unroll 1
-          for (int i = 0; i < D / 32; ++i) {
-            tc::tmem_ld32(o_addr + i * 32, s2);
-            tc::tmem_wait_ld(s2);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) s2[k] = __float_as_uint(__uint_as_float(s2[k]) * al);
-            tc::tmem_st32(o_addr + i * 32, s2);
+        const bool grow = mx > m_run + kGrow;
+        if (!begun || __any_sync(0xffffffffu, grow)) {
+          float al = 1.f;
+          if (grow) {
+            al = ex2(m_run - mx);  // (0 while nothing was seen)
+            m_run = mx;
           }
+          l2[0] = __fmul2_rn(l2[0], make_float2(al, al));
+          l2[1] = __fmul2_rn(l2[1], make_float2(al, al));
+          lh[0] = lh[1] = make_float2(0.f, 0.f);
+          if (begun) {
+            // (S of this tile was issued behind P V of the last one: O is complete)
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) {
+              tc::tmem_ld32(o_addr + i * 32, w);
+              tc::tmem_wait_ld(w);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * al);
+              tc::tmem_st32(o_addr + i * 32, w);
+            }
+          }
+          uint32_t s0[32], s1[32];  // the first half again
+          tc::tmem_ld32(s_addr, s0);
+          tc::tmem_wait_ld(s0);
+          if (!plain) prepare(s0, 0);
+          weights(s0, mul, m_run, w, 0, lh);
+          tc::tmem_ld32(s_addr + 32, s1);
+          tc::tmem_wait_ld(s1);
+          if (!plain) prepare(s1, 1);
+          weights(s1, mul, m_run, w, 16, lh);
         }
         // Rows past the end in the last block hold stale data, and 0 x NaN
         // would poison O: tile A's warpgroup clears them before its first P V
-        const int tail = p.n % kBlockSize;
-        if (t == 0 && tail && p.n - kb < kKeys) {
+        if (t == 0 && left < kKeys && left % kBlockSize) {
           const int vi = 2 * step + 1;
           if (!wait_all(FULL(vi % NS), (vi / NS) & 1)) { ok = false; break; }
           unsigned char* const vt = sR + (vi % NS) * KT;
-          const int r0 = p.n - kb, nr = kBlockSize - tail;
+          const int nr = kBlockSize - left % kBlockSize;
           for (int i = col; i < nr * 8 * KB; i += kWg) {
-            const int h = i / (nr * 8), r = r0 + (i / 8) % nr;
+            const int h = i / (nr * 8), r = left + (i / 8) % nr;
             *reinterpret_cast<uint4*>(vt + h * HALF + r * 128 + ((i % 8) << 4)) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-          chunk(2 * h, s2);
-          weights(s2, mul, m_run, w, 0, l2);
-          chunk(2 * h + 1, s2);
-          weights(s2, mul, m_run, w, 16, l2);
-          store_p(s_addr + 32 * h, w);
-          tc::fence_before_sync();
-          mbar_arrive(TB(t, P0 + h));
-        }
+        store_p(s_addr, w);
+        tc::fence_before_sync();
+        mbar_arrive(TB(t, P0));
+        weights(s2, mul, m_run, w, 0, lh);
+        weights(s3, mul, m_run, w, 16, lh);
+        store_p(s_addr + 32, w);
+        tc::fence_before_sync();
+        mbar_arrive(TB(t, P0 + 1));
+        l2[0] = __fadd2_rn(l2[0], lh[0]);
+        l2[1] = __fadd2_rn(l2[1], lh[1]);
       }
       if (!ok) break;
       // ---- the piece's O
+      const CrossPiece p = walk.get();
       const float2 la = __fadd2_rn(l2[0], l2[1]);
       const float l_run = la.x + la.y;
       if (bad && lane == 0 && a.err_flag) atomicOr(a.err_flag, kErrBlockId);
       if (!wait_all(TB(t, ODONE), (on++) & 1)) { ok = false; break; }
       tc::fence_after_sync();
       const size_t pt = static_cast<size_t>(max(p.slot, 0)) * kTiles + t;
-      const float inv = 1.f / l_run;
+      // A piece of a cut item: if every other piece has stored its partial, this
+      // one is merged with them straight from tensor memory, else it is stored
+      // (most items are cut in two, and the part a share begins with is long done).
+      int first = blockIdx.x, pieces = 1;
+      bool store = false;
+      float wgt = 1.f, L = l_run, M = m_run;  // this piece's weight, the item's sum and maximum
+      bool zero = bad;
+      if (p.slot >= 0) {
+        cross_chain(s_total, p, &first, &pieces);
+        if (col == 0) s_total.old[t] = atomicAdd(a.count + 2 * first + t, 0u);
+        if (!group_sync()) { ok = false; break; }
+        store = s_total.old[t] != static_cast<unsigned>(pieces - 1);
+        if (!store) {
+          __threadfence();
+          for (int i = 0; i < pieces; ++i)
+            if (first + i != blockIdx.x) M = fmaxf(M, __ldcg(a.part_ml + cross_tile<kTiles>(first, i, t) * kCols + col).x);
+          L = 0.f;
+          for (int i = 0; i < pieces; ++i) {
+            const float2 ml = first + i == blockIdx.x
+                                  ? make_float2(m_run, bad ? -1.f : l_run)
+                                  : __ldcg(a.part_ml + cross_tile<kTiles>(first, i, t) * kCols + col);
+            zero |= ml.y < 0.f;
+            L = fmaf(cross_weight(ml.x, M), ml.y, L);
+          }
+          wgt = cross_weight(m_run, M);
+          if (col == 0) a.count[2 * first + t] = 0;
+        }
+      }
+      const float inv = 1.f / L;
 #pragma unroll 1
       for (int h = 0; h < KB; ++h) {
         __syncwarp();  // (the staging area has been read)
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 2; ++q) {
           uint32_t o[32];
           tc::tmem_ld32(o_addr + 64 * h + 32 * q, o);
           tc::tmem_wait_ld(o);
+          const int at = ((8 * h + 4 * q) * kCols + col) * 8;  // these dims in a partial
+          if (store) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (p.slot < 0) {
-              uint32_t v[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                v[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + i) ^ (lane & 7)) << 4)) =
-                  make_uint4(v[0], v[1], v[2], v[3]);
-            } else {
+            for (int i = 0; i < 4; ++i) {
               float v[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * i + e]);
-              cross_store8(a.part_o + pt * kCols * D + ((8 * h + 4 * q + i) * kCols + col) * 8, v);
+              cross_store8(a.part_o + pt * kCols * D + at + i * kCols * 8, v);
             }
+            continue;
+          }
+          if (pieces > 1) {
+            float acc[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+            for (int x = 0; x < pieces; ++x) {
+              if (first + x == blockIdx.x) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) acc[k] = fmaf(wgt, __uint_as_float(o[k]), acc[k]);
+                continue;
+              }
+              const size_t xt = cross_tile<kTiles>(first, x, t);
+              const float wx = cross_weight(__ldcg(a.part_ml + xt * kCols + col).x, M);
+              float4 v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                v[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + xt * kCols * D + at + i / 2 * kCols * 8) + i % 2);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                acc[4 * i] = fmaf(wx, v[i].x, acc[4 * i]);
+                acc[4 * i + 1] = fmaf(wx, v[i].y, acc[4 * i + 1]);
+                acc[4 * i + 2] = fmaf(wx, v[i].z, acc[4 * i + 2]);
+                acc[4 * i + 3] = fmaf(wx, v[i].w, acc[4 * i + 3]);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(acc[k]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + i) ^ (lane & 7)) << 4)) =
+                make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
-        if (p.slot < 0) {
+        if (!store) {
           __syncwarp();
-          put_rows(64 * h, bad);
+          put_rows(p, 64 * h, zero);
         }
       }
       tc::fence_before_sync();  // (O has been read before this warpgroup's next P lets it be written)
-      if (p.slot >= 0) {
+      if (store) {
         a.part_ml[pt * kCols + col] = make_float2(m_run, bad ? -1.f : l_run);
-        int first, pieces;
-        cross_chain(s_total, p, &first, &pieces);
         __threadfence();
         if (!group_sync()) { ok = false; break; }
         if (col == 0) s_total.old[t] = atomicInc(a.count + 2 * first + t, pieces - 1);
