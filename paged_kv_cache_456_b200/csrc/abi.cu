@@ -899,6 +899,9 @@ pa_status pa_cross_attention(void* out, const void* q, const void* k_cache, cons
   if (dtype == PA_BF16 && ((st = encode_cache_map(&a.tm_k, k_cache, rows, head_dim)) != PA_OK ||
                            (st = encode_cache_map(&a.tm_v, v_cache, rows, head_dim)) != PA_OK))
     return st;
+  if (k.tma_q && !pa::encode_prefill_out_map(&a.tm_q, const_cast<void*>(q), num_query_tokens,
+                                             num_q_heads, head_dim, num_q_heads / num_kv_heads))
+    return PA_ERR_CUDA;
   if (pa::launch_cross_attention(a, k, dev.sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return PA_ERR_CUDA;

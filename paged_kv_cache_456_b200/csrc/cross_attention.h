@@ -55,6 +55,7 @@ struct CrossArgs {
   float* part_o;               // [slots][column tiles][D / 8][columns of a tile][8]
   CUtensorMap tm_k;            // bf16: caches as [num_blocks * Hkv * 16][D], boxes 16 x 64, SW128
   CUtensorMap tm_v;
+  CUtensorMap tm_q;            // (where the kernel asks) q as (D, query heads, rows), boxes 64 x G x 128 / G
 };
 
 // A kernel and how it cuts the work.
@@ -63,6 +64,7 @@ struct CrossKernel {
   int threads, ctas_per_sm;
   size_t smem;                 // dynamic shared memory of a CTA
   int cols, keys;              // columns of an item, keys of a tile
+  bool tma_q;                  // reads q through tm_q
 };
 // The kernel for a call (host-known sizes only).
 CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes);
@@ -111,7 +113,7 @@ struct CrossTotal {
   long long W;       // tiles of the call
   int workers;       // workers that have some
   unsigned old[2];   // partials stored before this one, per column tile
-  long long scratch[40];
+  long long scratch[16];  // (a long long per warp, two more; at most 14 warps)
 };
 
 // Lays the work out; every thread of the CTA takes part.
@@ -193,9 +195,13 @@ struct CrossPiece {
   int s, kvh, grp;   // sequence, KV head, group of columns
   int t0, t1, nt;    // tiles [t0, t1) of the item's nt
   int n, live;       // keys, live columns of the group
-  long long base;    // column 0 of the group in q and out, in rows of D elements
+  int row;           // query row of column 0
   int slot;          // partial slot, or -1: the whole item
   long long begin;   // the item's first tile
+  // column 0 of the group in q and out, in rows of D elements
+  __device__ __forceinline__ long long base(const CrossArgs& a) const {
+    return static_cast<long long>(row) * a.num_q_heads + (kvh << a.group_log2);
+  }
 };
 
 // The pieces of a share, in order.
@@ -221,11 +227,12 @@ struct CrossWalk {
     p->n = m.z;
     const int c0 = p->grp * cols;
     p->live = min(cols, (m.y << a.group_log2) - c0);
-    p->base = static_cast<long long>(m.x + (c0 >> a.group_log2)) * a.num_q_heads + (p->kvh << a.group_log2);
+    p->row = m.x + (c0 >> a.group_log2);
     p->nt = cross_tiles(m.z, keys);
     p->t0 = x.tile;
     p->t1 = min(p->nt, x.tile + x.left);
-    p->slot = x.tile > 0 ? 2 * blockIdx.x : p->t1 < p->nt ? 2 * blockIdx.x + 1 : -1;
+    const int w = blockIdx.x;
+    p->slot = x.tile > 0 ? 2 * w : p->t1 < p->nt ? 2 * w + 1 : -1;
     p->begin = x.at - x.tile;
     x.at += p->t1 - p->t0;
     x.left -= p->t1 - p->t0;
@@ -359,7 +366,7 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
       const float inv = 1.f / L[u];
 #pragma unroll
       for (int d = 0; d < 4; ++d) acc[u][d] = bad[u] ? 0.f : acc[u][d] * inv;
-      cross_store4(static_cast<T*>(a.out) + (p.base + cross_column(a, t * COLS + c[u])) * D + ch[u] * 4, acc[u]);
+      cross_store4(static_cast<T*>(a.out) + (p.base(a) + cross_column(a, t * COLS + c[u])) * D + ch[u] * 4, acc[u]);
     }
   }
 }

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
 
   // ---- this warp's loads: blocks t0 + warp, + 8, ... of every piece with keys
   CrossWalk ahead(a, share, COLS);
-  CrossPiece ip;
+  CrossPiece ip{};
   bool more = true;
   int ib = 0, iend = 0, issued = 0;
   int ids = 0, id_first = 0;                // lane l: the id of block id_first + 8 l
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
     if (p.n == 0) {
       for (int i = tid; i < p.live * (D / 8); i += kThreads)
         reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
-                                 (p.base + cross_column(a, i / (D / 8))) * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
+                                 (p.base(a) + cross_column(a, i / (D / 8))) * D)[i % (D / 8)] = make_uint4(0, 0, 0, 0);
       continue;
     }
     // q of column 8 nt + g as the B operand (dims 2 tq, + 1 and 2 tq + 8, + 9 of
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
       for (int i = tid; i < NT * MT * 32; i += kThreads) {
         const int nt = i / (MT * 32), k = i / 32 % MT;
         const uint32_t* src = reinterpret_cast<const uint32_t*>(
-            static_cast<const __nv_bfloat16*>(a.q) + (p.base + cross_column(a, min(8 * nt + g, p.live - 1))) * D) + tq;
+            static_cast<const __nv_bfloat16*>(a.q) + (p.base(a) + cross_column(a, min(8 * nt + g, p.live - 1))) * D) + tq;
         s_q[i] = make_uint2(__ldg(src + 8 * k), __ldg(src + 8 * k + 4));
       }
       __syncthreads();
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
 #pragma unroll
     for (int nt = 0; nt < (Q_SMEM ? 0 : NT); ++nt) {
       const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          static_cast<const __nv_bfloat16*>(a.q) + (p.base + cross_column(a, min(8 * nt + g, p.live - 1))) * D) + tq;
+          static_cast<const __nv_bfloat16*>(a.q) + (p.base(a) + cross_column(a, min(8 * nt + g, p.live - 1))) * D) + tq;
 #pragma unroll
       for (int k = 0; k < MT; ++k) {
         qb[nt][k][0] = __ldg(src + 8 * k);
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
           const float inv = 1.f / L;
 #pragma unroll
           for (int d = 0; d < 8; ++d) acc[d] = any ? 0.f : acc[d] * inv;
-          cross_store8(static_cast<__nv_bfloat16*>(a.out) + (p.base + cross_column(a, 8 * nt + c)) * D + 8 * ch, acc);
+          cross_store8(static_cast<__nv_bfloat16*>(a.out) + (p.base(a) + cross_column(a, 8 * nt + c)) * D + 8 * ch, acc);
         } else {
           cross_store8(a.part_o + static_cast<size_t>(p.slot) * COLS * D + (ch * COLS + 8 * nt + c) * 8, acc);
           if (ch == 0) a.part_ml[static_cast<size_t>(p.slot) * COLS + 8 * nt + c] = make_float2(M, any ? -1.f : L);

@@ -55,7 +55,7 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
     if (p.n == 0) {
       for (int c = tid / 16; c < kCols; c += kThreads / 16) {
         if (c >= p.live) break;
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + (p.base + cross_column(a, c)) * D);
+        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + (p.base(a) + cross_column(a, c)) * D);
         for (int i = tid & 15; i < CPR; i += 16) dst[i] = make_float4(0.f, 0.f, 0.f, 0.f);
       }
       continue;
@@ -78,7 +78,7 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
     __syncthreads();  // (the last piece's Q, K and V have been read)
     for (int i = tid; i < kCols * CPR; i += kThreads) {
       const int c = i / CPR, k = i % CPR;
-      const long long x = p.base + cross_column(a, min(c, p.live - 1));
+      const long long x = p.base(a) + cross_column(a, min(c, p.live - 1));
       cp_async16(smem_addr(sQ + c * D + 4 * (k ^ ((c >> 3) & 7))), static_cast<const float*>(a.q) + x * D + 4 * k,
                  c < p.live);
     }
@@ -192,7 +192,7 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
       for (int off = 8; off; off >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
       const int c = cg * 8 + i;
       if (c >= p.live) continue;
-      const long long x = p.base + cross_column(a, c);
+      const long long x = p.base(a) + cross_column(a, c);
       const float inv = p.slot < 0 ? 1.f / l[i] : 1.f;
 #pragma unroll
       for (int j = 0; j < DJ; ++j) {

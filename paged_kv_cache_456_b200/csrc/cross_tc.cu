@@ -21,14 +21,19 @@
 //                   at a piece's end: one tile's softmax always runs beside
 //                   the other's MMAs.  P is handed over in halves of 64 keys,
 //                   so that its product starts half a softmax early;
-//   warps 10, 11    the q rows of tile A, of tile B, of the next piece as soon
-//                   as this piece's last scores are computed.
+//   warp 10         the q rows of each next piece, once its last scores are done
+//                   (warp 11 completes the third warpgroup).
 // The softmax of a tile takes the last running maximum on trust: the first
 // half's weights are computed while the tile's own maximum is, and computed
 // again in the rare case that it exceeds the running one by 2^8 or more.
-// The output leaves through a staging area of the warp, so that stores (as
-// the q loads) touch whole rows: one row per lane and instruction cost 2000
-// cycles a tile in the load-store unit, and delayed what was queued behind.
+// The output leaves through a staging area of the warp, so that stores touch
+// whole rows: one row per lane and instruction cost 2000 cycles a tile in the
+// load-store unit, and delayed what was queued behind.
+// Tried and slower (4 x 4096 x 4096, 32 heads; this form 0.90 ms): S in two
+// buffers of 64 keys a tile, whose MMAs cost a third more operand traffic (0.96
+// to 1.25 ms); an MMA warp for each tile, whose softmaxes then fall into step
+// (1.03 ms); an eighth to a half of the weights from a cubic on the FMA units
+// (0.94 to 0.99 ms).
 // A piece with at most 128 columns leaves tile B out.  Every mbarrier wait is
 // bounded; a wait that runs out sets PA_ERRBIT_TIMEOUT and every role leaves.
 #include <cstdint>
@@ -48,7 +53,7 @@ namespace {
 constexpr int kCols = 128, kTiles = 2, kKeys = 128;
 constexpr int kBlocks = kKeys / kBlockSize;  // blocks of a K/V tile
 constexpr int kWg = 128;                     // threads of a softmax warpgroup
-constexpr int kProducerWarp = 8, kMmaWarp = 9, kThreads = 384;
+constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kThreads = 384;
 // registers: 168 a thread at launch (384 x 168 = 64512), then 192 for the two
 // softmax warpgroups and 120 for the third (256 x 192 + 128 x 120 = 64512)
 constexpr int kRegsSoftmax = 192, kRegsRest = 120;
@@ -100,11 +105,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, bool fill) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0)
-               : "memory");
+// a 3-D tensor load (coordinate x a multiple of 16 bytes' worth of elements)
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
-
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       mbar_init(TB(t, P0), kWg);
       mbar_init(TB(t, P0 + 1), kWg);
       mbar_init(TB(t, ODONE), 1);
-      mbar_init(TB(t, QFULL), 32);
+      mbar_init(TB(t, QFULL), 1);
       mbar_init(TB(t, QEMPTY), 1);
       mbar_init(TB(t, SYNC), kWg);
     }
@@ -378,35 +386,35 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       if (tc::elect_one()) tc::commit(DRAIN);
       wait_all(DRAIN, 0);
       __syncwarp();
-    } else {
-      // ---------------- q rows of tile t, whole rows at a time --------------------------
-      const int t = warp - kMmaWarp - 1;
-      int qn = 0;
+    } else if (warp == kQWarp) {
+      // ---------------- q rows: 128 / G rows x G heads a tile, by tensor loads (columns past
+      // the sequence's last get other rows, or zeros past the tensor's end) -------------
+      int qn[kTiles] = {0, 0};
       bool ok = true;
-      while (walk.next(a, true)) {
+      const int rows = kCols >> a.group_log2;
+      while (ok && walk.next(a, true)) {
         const CrossPiece p = walk.get();
-        if (t >= live_tiles(p)) continue;
-        if (aborted() || (qn > 0 && !wait_all(TB(t, QEMPTY), (qn - 1) & 1))) {
-          ok = false;
-          break;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if (t >= live_tiles(p) || !ok) continue;
+          if (aborted() || (qn[t] > 0 && !wait_all(TB(t, QEMPTY), (qn[t] - 1) & 1))) {
+            ok = false;
+            continue;
+          }
+          ++qn[t];
+          if (lane == 0) {
+            mbar_arrive_expect_tx(TB(t, QFULL), QT);
+#pragma unroll
+            for (int h = 0; h < KB; ++h)
+              tma_load_3d(smem_addr(sQ + t * QT) + h * (kCols * 128), &a.tm_q, h * 64, p.kvh << a.group_log2,
+                          p.row + t * rows, TB(t, QFULL));
+          }
+          __syncwarp();
         }
-        ++qn;
-        const uint32_t qb = smem_addr(sQ + t * QT);
-        constexpr int CPR = D / 8;  // 16-byte chunks of a row
-        const int k = lane % CPR, c0 = lane / CPR;
-        const __nv_bfloat16* const src = static_cast<const __nv_bfloat16*>(a.q) + p.base * D + k * 8;
-        const int live = p.live - t * kCols;
-#pragma unroll 4
-        for (int i = 0; i < kCols; i += 32 / CPR) {
-          const int c = c0 + i;
-          cp_async16_zfill(qb + (k / 8) * (kCols * 128) + c * 128 + (((k ^ c) & 7) << 4),
-                           src + cross_column(a, t * kCols + min(c, live - 1)) * D, c < live);
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        mbar_arrive(TB(t, QFULL));
       }
       if (!ok) timeout();
+      for (int t = 0; t < kTiles; ++t)  // (the last loads land before the CTA can exit)
+        if (qn[t] > 0) wait_all(TB(t, QFULL), (qn[t] - 1) & 1);
     }
   } else {
     regs_inc<kRegsSoftmax>();
@@ -429,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       // the staging area (chunk i of row r at i ^ (r % 8)) or zeros
       auto put_rows = [&](const CrossPiece& p, int base, bool zeros) {
         const int i = lane % 8;
-        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.out) + p.base * D + base + 8 * i;
+        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.out) + p.base(a) * D + base + 8 * i;
         const int c0 = t * kCols + (warp % 4) * 32 + lane / 8;
         uint4 v[8];
 #pragma unroll
@@ -690,6 +698,7 @@ CrossKernel info() {
   k.smem = Shape<D>::SMEM;
   k.cols = kTiles * kCols;
   k.keys = kKeys;
+  k.tma_q = true;
   return k;
 }
 
