@@ -139,19 +139,48 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
-def _same_device(ref: torch.Tensor, **others: Optional[torch.Tensor]) -> None:
-    """Every tensor on ``ref``'s CUDA device (a host pointer would fault in the kernel)."""
-    dev = ref.device
-    if dev.type != "cuda":
+# The entry points below check every tensor that they hand on.  At a few
+# microseconds of device time a call, the checks are kept cheap: device indexes
+# rather than device objects, no context manager when the device is current.
+def _one_device(ref: torch.Tensor, names: str, *others: Optional[torch.Tensor]) -> int:
+    """The index of ``ref``'s CUDA device, which every other tensor must be on (a host pointer
+    would fault in the kernel); ``names`` are theirs."""
+    dev = ref.get_device()
+    if dev < 0:
         raise ValueError("libpa works on CUDA tensors")
-    for name, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            name = next(n for n, o in zip(names.split(), others) if o is t)
+            raise ValueError(f"{name} is on {t.device}, not on {ref.device}")
+    return dev
+
+
+def _call_on(dev: int, fn, what: str, stream, args: tuple) -> None:
+    """``fn(*args, stream)`` with device ``dev`` current, on its current stream by default."""
+    if stream is None:
+        stream = _raw_stream(dev)
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != PA_OK:
+        raise PagedAttentionError(status, what)
+
+
+def _raw_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+# (the handle without a Stream object around it, where this torch has it)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _rows_ptr(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype):
     """(pointer, elements between tokens) of ``[T][H][D]`` rows whose heads lie side by side."""
-    if t.shape != shape or t.dtype != dtype:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, "
                          f"not {t.dtype} of shape {tuple(t.shape)}")
     T, H, D = shape
@@ -162,7 +191,7 @@ def _rows_ptr(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype):
 
 
 def _array_ptr(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> int:
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)}, "
                          f"not {t.dtype} of shape {tuple(t.shape)}")
     return t.data_ptr()
@@ -303,9 +332,9 @@ def cross_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     """Attention of each sequence's rows of ``q`` ``[T][Hq][D]`` (rows ``query_start[s]`` to
     ``query_start[s+1]``) to all ``context_lens[s]`` tokens of its block table, into ``out``;
     see ``pa_cross_attention``."""
-    _same_device(q, out=out, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-                 context_lens=context_lens, query_start=query_start, workspace=workspace,
-                 err_flag=err_flag)
+    dev = _one_device(q, "out k_cache v_cache block_tables context_lens query_start workspace err_flag",
+                      out, k_cache, v_cache, block_tables, context_lens, query_start, workspace,
+                      err_flag)
     if q.dim() != 3 or k_cache.dim() != 4 or block_tables.dim() != 2:
         raise ValueError("q is [rows][heads][head_dim], the caches [blocks][heads][16][head_dim], "
                          "block_tables [sequences][blocks]")
@@ -324,11 +353,9 @@ def cross_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     err = None if err_flag is None else _array_ptr("err_flag", err_flag, err_flag.shape, i32)
-    with torch.cuda.device(q.device):
-        _check(library().pa_cross_attention(
-            *args, S, T, Hq, Hkv, D, bs, B, N, int(max_context_len), scale, code,
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), err,
-            _stream(stream)), "pa_cross_attention")
+    _call_on(dev, library().pa_cross_attention, "pa_cross_attention", stream,
+             args + (S, T, Hq, Hkv, D, bs, B, N, int(max_context_len), scale, code,
+                     workspace.data_ptr(), workspace.nbytes, err))
     return out
 
 
@@ -386,9 +413,9 @@ def rope_append(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
         raise ValueError("key, value, k_cache, v_cache and slot_mapping go together")
     if ref.dim() != 3:
         raise ValueError("q and key are [tokens][heads][head_dim]")
-    _same_device(ref, q_out=q_out, key=key, value=value, k_cache=k_cache, v_cache=v_cache,
-                 slot_mapping=slot_mapping, positions=positions, inv_freq=inv_freq,
-                 pair_axis=pair_axis, err_flag=err_flag)
+    dev = _one_device(ref, "q_out key value k_cache v_cache slot_mapping positions inv_freq pair_axis err_flag",
+                      q_out, key, value, k_cache, v_cache, slot_mapping, positions, inv_freq,
+                      pair_axis, err_flag)
     T, _, D = ref.shape
     dt = ref.dtype
     code = _dtype_code(ref)
@@ -411,11 +438,9 @@ def rope_append(q_out: Optional[torch.Tensor], q: Optional[torch.Tensor],
         vc = _array_ptr("v_cache", v_cache, (N, Hkv, bs, D), dt)
         slots = _array_ptr("slot_mapping", slot_mapping, (T,), torch.int64)
     err = None if err_flag is None else _array_ptr("err_flag", err_flag, err_flag.shape, torch.int32)
-    with torch.cuda.device(ref.device):
-        _check(library().pa_rope_append(
-            op, qp, kp, vp, kc, vc, slots, pos, freq, axis, axes, 2 * half, int(adjacent),
-            rot_scale, os_, qs, ks, vs, T, Hq, Hkv, D, bs, N, code, err, _stream(stream)),
-            "pa_rope_append")
+    _call_on(dev, library().pa_rope_append, "pa_rope_append", stream,
+             (op, qp, kp, vp, kc, vc, slots, pos, freq, axis, axes, 2 * half, int(adjacent),
+              rot_scale, os_, qs, ks, vs, T, Hq, Hkv, D, bs, N, code, err))
     return q_out
 
 
