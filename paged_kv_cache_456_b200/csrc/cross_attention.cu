@@ -25,9 +25,9 @@ std::map<std::pair<int, const void*>, bool> g_ready;  // (device, kernel): its s
 }  // namespace
 
 CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes) {
-  if (elem_bytes == 4) return cross_simt_kernel_info(head_dim);
   const long long columns =
       num_seqs > 0 ? (static_cast<long long>(num_rows) * group + num_seqs - 1) / num_seqs : 0;
+  if (elem_bytes == 4) return cross_simt_kernel_info(head_dim, columns);
   if (columns <= kFewColumns) return cross_few_kernel_info(head_dim, static_cast<int>(columns));
   return cross_tc_kernel_info(head_dim);
 }

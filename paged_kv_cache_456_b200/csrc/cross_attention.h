@@ -68,8 +68,9 @@ struct CrossKernel {
 };
 // The kernel for a call (host-known sizes only).
 CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes);
-CrossKernel cross_simt_kernel_info(int head_dim);  // fp32, CUDA cores (cross_simt.cu)
-CrossKernel cross_tc_kernel_info(int head_dim);    // bf16, many columns: tcgen05 (cross_tc.cu)
+// fp32, about `columns` query columns a (sequence, KV head): CUDA cores (cross_simt.cu)
+CrossKernel cross_simt_kernel_info(int head_dim, long long columns);
+CrossKernel cross_tc_kernel_info(int head_dim);  // bf16, many columns: tcgen05 (cross_tc.cu)
 // bf16, about `columns` (at most 32) query columns a (sequence, KV head): mma.sync (cross_few.cu)
 CrossKernel cross_few_kernel_info(int head_dim, int columns);
 
@@ -82,6 +83,10 @@ CrossLayout cross_layout(const CrossKernel& k, int head_dim, int num_sms);
 cudaError_t launch_cross_attention(CrossArgs& a, const CrossKernel& k, int num_sms, cudaStream_t stream);
 
 #ifdef __CUDACC__
+__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ int cross_tiles(int n, int keys) { return n > 0 ? (n + keys - 1) / keys : 1; }
 
 // Sequence s's {first row, rows, keys, groups of `cols` columns}, checked: one
@@ -116,23 +121,39 @@ struct CrossTotal {
   long long scratch[16];  // (a long long per warp, two more; at most 14 warps)
 };
 
-// Lays the work out; every thread of the CTA takes part.
+// Lays the work out; every thread of the CTA takes part, and is past a
+// __syncthreads at the end.  Up to 128 sequences every warp does it for itself
+// (a lane has up to four, whose lengths it loads together); more are spread
+// over the CTA.
 template <int THREADS>
 __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, int keys, CrossTotal* total) {
   long long* const scratch = total->scratch;
-  constexpr int WARPS = THREADS / 32;
+  constexpr int WARPS = THREADS / 32, MINE = 4;
   const int tid = threadIdx.x, lane = tid & 31, S = a.num_seqs;
-  const int per = (S + THREADS - 1) / THREADS;
-  const int s0 = min(S, tid * per), s1 = min(S, s0 + per);
+  const bool by_warp = S <= 32 * MINE;
+  const int parts = by_warp ? 32 : THREADS, part = by_warp ? lane : tid;
+  const int per = (S + parts - 1) / parts;
+  const int s0 = min(S, part * per), s1 = min(S, s0 + per);
   auto tiles_of = [&](const int4& m) -> long long {
     return static_cast<long long>(a.num_kv_heads) * m.w * cross_tiles(m.z, keys);
   };
   long long local = 0;
   int bits = 0;
-  for (int s = s0; s < s1; ++s) {
-    int bit;
-    local += tiles_of(cross_seq(a, s, cols, &bit));
-    bits |= bit;
+  int4 mine[MINE];  // (by_warp)
+  if (by_warp) {
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+      int bit = 0;
+      mine[k] = s0 + k < s1 ? cross_seq(a, s0 + k, cols, &bit) : make_int4(0, 0, 0, 0);
+      local += tiles_of(mine[k]);
+      bits |= bit;
+    }
+  } else {
+    for (int s = s0; s < s1; ++s) {
+      int bit;
+      local += tiles_of(cross_seq(a, s, cols, &bit));
+      bits |= bit;
+    }
   }
   if (bits && blockIdx.x == 0 && a.err_flag) atomicOr(a.err_flag, bits);
   long long incl = local;
@@ -141,15 +162,20 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
     const long long t = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += t;
   }
-  if (lane == 31) scratch[tid >> 5] = incl;
-  __syncthreads();
-  CrossShare x;
-  long long run = incl - local, W = 0;
+  long long run = incl - local, W;
+  if (by_warp) {
+    W = __shfl_sync(0xffffffffu, incl, 31);
+  } else {
+    if (lane == 31) scratch[tid >> 5] = incl;
+    __syncthreads();
+    W = 0;
 #pragma unroll
-  for (int i = 0; i < WARPS; ++i) {
-    if (i < (tid >> 5)) run += scratch[i];
-    W += scratch[i];
+    for (int i = 0; i < WARPS; ++i) {
+      if (i < (tid >> 5)) run += scratch[i];
+      W += scratch[i];
+    }
   }
+  CrossShare x;
   const int w = blockIdx.x;
   const int workers = static_cast<int>(max(1LL, min(static_cast<long long>(gridDim.x), W)));
   // (64-bit division costs hundreds of cycles: only where it is needed)
@@ -165,28 +191,49 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
     total->W = W;
     total->workers = workers;
   }
-  int* const res = reinterpret_cast<int*>(scratch + WARPS);
-  if (run <= x.at && x.at < run + local) {  // (one thread's sequences hold the first tile)
-    long long off = x.at - run;
-    for (int s = s0; s < s1; ++s) {
-      int bit;
-      const int4 m = cross_seq(a, s, cols, &bit);
-      const long long t = tiles_of(m);
-      if (off < t) {
-        const int nt = cross_tiles(m.z, keys);
-        const int item = off < (1LL << 31) ? static_cast<int>(off) / nt : static_cast<int>(off / nt);
-        res[0] = s;
-        res[1] = item;
-        res[2] = static_cast<int>(off - static_cast<long long>(item) * nt);
-        break;
-      }
+  // one part's sequences hold the first tile
+  const bool owner = run <= x.at && x.at < run + local;
+  long long off = x.at - run;
+  int fs = 0, fitem = 0, ftile = 0;
+  auto place = [&](int s, const int4& m) -> bool {
+    const long long t = tiles_of(m);
+    if (off >= t) {
       off -= t;
+      return false;
     }
+    const int nt = cross_tiles(m.z, keys);
+    fs = s;
+    fitem = off < (1LL << 31) ? static_cast<int>(off) / nt : static_cast<int>(off / nt);
+    ftile = static_cast<int>(off - static_cast<long long>(fitem) * nt);
+    return true;
+  };
+  if (by_warp) {
+    bool done = !owner;
+#pragma unroll
+    for (int k = 0; k < MINE; ++k)
+      if (!done) done = place(s0 + k, mine[k]);
+    const unsigned who = __ballot_sync(0xffffffffu, owner);
+    const int src = who ? __ffs(who) - 1 : 0;
+    x.s = __shfl_sync(0xffffffffu, fs, src);
+    x.item = __shfl_sync(0xffffffffu, fitem, src);
+    x.tile = __shfl_sync(0xffffffffu, ftile, src);
+    __syncthreads();
+  } else {
+    int* const res = reinterpret_cast<int*>(scratch + WARPS);
+    if (owner) {
+      for (int s = s0; s < s1; ++s) {
+        int bit;
+        if (place(s, cross_seq(a, s, cols, &bit))) break;
+      }
+      res[0] = fs;
+      res[1] = fitem;
+      res[2] = ftile;
+    }
+    __syncthreads();
+    x.s = res[0];
+    x.item = res[1];
+    x.tile = res[2];
   }
-  __syncthreads();
-  x.s = res[0];
-  x.item = res[1];
-  x.tile = res[2];
   return x;
 }
 
@@ -309,6 +356,38 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
                                             int i0, int team) {
   const int live = min(COLS, p.live - t * COLS);
   const int units = live * (D / 4);
+  if (pieces <= 16 && units * 16 <= team) {
+    // few units: 16 lanes of one, a piece each, summed by a fixed tree
+    const int u = i0 / 16, j = i0 % 16;
+    const int x = min(u, units - 1), ch = x / (2 * live) * 2 + (x & 1), c = x % (2 * live) >> 1;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j < pieces) {
+      const size_t pt = cross_tile<TILES>(first, j, t);
+      ml = __ldcg(a.part_ml + pt * COLS + c);
+      o = __ldcg(reinterpret_cast<const float4*>(a.part_o + pt * COLS * D + (ch / 2 * COLS + c) * 8 + (ch & 1) * 4));
+    }
+    float M = ml.x;
+#pragma unroll
+    for (int k = 8; k; k >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, k));
+    const float w = cross_weight(ml.x, M);
+    float v[5] = {w * o.x, w * o.y, w * o.z, w * o.w, w * ml.y};
+    int bad = ml.y < 0.f;
+#pragma unroll
+    for (int k = 8; k; k >>= 1) {
+#pragma unroll
+      for (int d = 0; d < 5; ++d) v[d] += __shfl_xor_sync(0xffffffffu, v[d], k);
+      bad |= __shfl_xor_sync(0xffffffffu, bad, k);
+    }
+    if (j == 0 && u < units) {
+      const float inv = 1.f / v[4];
+      float r[4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) r[d] = bad ? 0.f : v[d] * inv;
+      cross_store4(static_cast<T*>(a.out) + (p.base(a) + cross_column(a, t * COLS + c)) * D + ch * 4, r);
+    }
+    return;
+  }
   for (int u0 = i0; u0 < units; u0 += UNITS * team) {
     int c[UNITS], ch[UNITS];
     float M[UNITS], L[UNITS], acc[UNITS][4];
@@ -367,6 +446,84 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
 #pragma unroll
       for (int d = 0; d < 4; ++d) acc[u][d] = bad[u] ? 0.f : acc[u][d] * inv;
       cross_store4(static_cast<T*>(a.out) + (p.base(a) + cross_column(a, t * COLS + c[u])) * D + ch[u] * 4, acc[u]);
+    }
+  }
+}
+
+// The same by a whole CTA of `team` threads with room for the pieces' weights
+// in shared memory (kMergeFloats<COLS>): a column's maximum,
+// weights and sum are worked out once, and the pass over the partials holds
+// nothing but them in flight.
+constexpr int kMergeSharedPieces = 31;
+template <int COLS>
+constexpr int kMergeFloats = (2 * kMergeSharedPieces + 1) * COLS;
+template <typename T, int D, int COLS, int UNITS, int AHEAD>
+__device__ __forceinline__ void cross_merge_shared(const CrossArgs& a, const CrossPiece& p, int first, int pieces,
+                                                   int i0, int team, float* s) {
+  float* const s_w = s;                                   // [pieces][COLS]: maximum, then weight
+  float* const s_l = s_w + kMergeSharedPieces * COLS;     // [pieces][COLS]
+  float* const s_inv = s_l + kMergeSharedPieces * COLS;   // [COLS]: 1 / sum, -1: poisoned
+  const int live = p.live;
+  for (int i = i0; i < pieces * COLS; i += team) {
+    const float2 ml = __ldcg(a.part_ml + cross_tile<1>(first, i / COLS, 0) * COLS + i % COLS);
+    s_w[i] = ml.x;
+    s_l[i] = ml.y;
+  }
+  __syncthreads();
+  for (int c = i0; c < live; c += team) {
+    float M = -INFINITY, L = 0.f;
+    bool bad = false;
+    for (int j = 0; j < pieces; ++j) M = fmaxf(M, s_w[j * COLS + c]);
+    for (int j = 0; j < pieces; ++j) {
+      const float w = cross_weight(s_w[j * COLS + c], M), l = s_l[j * COLS + c];
+      bad |= l < 0.f;
+      L = fmaf(w, l, L);
+      s_w[j * COLS + c] = w;
+    }
+    s_inv[c] = bad ? -1.f : 1.f / L;
+  }
+  __syncthreads();
+  const int units = live * (D / 4);
+  for (int u0 = i0; u0 < units; u0 += UNITS * team) {
+    int c[UNITS], ch[UNITS];
+    float acc[UNITS][4];
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      const int x = min(u0 + u * team, units - 1);  // (a repeat is stored twice, alike)
+      ch[u] = x / (2 * live) * 2 + (x & 1);         // (the two chunks of a stored 8 side by side)
+      c[u] = x % (2 * live) >> 1;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) acc[u][d] = 0.f;
+    }
+    for (int j0 = 0; j0 < pieces; j0 += AHEAD) {
+      float4 o[AHEAD][UNITS];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (j0 + j >= pieces) break;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+          o[j][u] = __ldcg(reinterpret_cast<const float4*>(a.part_o + cross_tile<1>(first, j0 + j, 0) * COLS * D +
+                                                           (ch[u] / 2 * COLS + c[u]) * 8 + (ch[u] & 1) * 4));
+      }
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (j0 + j >= pieces) break;
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u) {
+          const float w = s_w[(j0 + j) * COLS + c[u]];
+          acc[u][0] = fmaf(w, o[j][u].x, acc[u][0]);
+          acc[u][1] = fmaf(w, o[j][u].y, acc[u][1]);
+          acc[u][2] = fmaf(w, o[j][u].z, acc[u][2]);
+          acc[u][3] = fmaf(w, o[j][u].w, acc[u][3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UNITS; ++u) {
+      const float inv = s_inv[c[u]];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) acc[u][d] = inv == -1.f ? 0.f : acc[u][d] * inv;
+      cross_store4(static_cast<T*>(a.out) + (p.base(a) + cross_column(a, c[u])) * D + ch[u] * 4, acc[u]);
     }
   }
 }

@@ -67,6 +67,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
   const uint32_t slot0 = smem_addr(sm) + warp * DEPTH * C::SLOT;
 
   if (lane == 0) {
+    if (warp == 0) {
+      prefetch_tensormap(&a.tm_k);
+      prefetch_tensormap(&a.tm_v);
+    }
     for (int i = 0; i < DEPTH; ++i) mbar_init(full0 + 8 * i, 1);
     if (warp == 0) s_abort = 0;
     fence_barrier_init();
@@ -339,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
       __syncthreads();
       if (s_total.old[0] == static_cast<unsigned>(pieces - 1)) {
         __threadfence();
-        cross_merge<__nv_bfloat16, D, COLS, 1, 1, 8>(a, p, first, pieces, 0, tid, kThreads);
+        cross_merge<__nv_bfloat16, D, COLS, 1, 1, 4>(a, p, first, pieces, 0, tid, kThreads);
       }
     }
   }

@@ -208,6 +208,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
+    prefetch_tensormap(&a.tm_k);
+    prefetch_tensormap(&a.tm_v);
+    prefetch_tensormap(&a.tm_q);
     for (int i = 0; i < NS; ++i) {
       mbar_init(FULL(i), 1);
       mbar_init(EMPTY(i), 1);

@@ -21,7 +21,7 @@
 // Two kernels.  Where a row's units divide a warp (every power-of-two head_dim
 // up to 512 bf16 or 256 fp32 elements, with any rotary_dim that leaves whole
 // units), a warp takes a token, or a slice of its rows: a lane keeps the same
-// place in every row, its angles in registers, and four rows in flight; no
+// place in every row, its angles in registers, and three rows in flight; no
 // division, no barrier.  Other shapes take a CTA per few tokens, its units laid
 // end to end, angles read from shared memory per unit.  Measured on what both
 // can do, 16384 tokens of 48 rows of 256 bytes (402 MB): 67 us (91 %
