@@ -27,7 +27,7 @@ constexpr int kKeys = 64, kThreads = 128;
 
 // CTAs an SM, by shared memory and registers
 template <int D, int CPT>
-constexpr int kCtas = D == 64 ? (CPT == 8 ? 2 : CPT == 4 ? 4 : 5) : (CPT <= 2 ? 3 - (CPT == 2) : 2);
+constexpr int kCtas = D == 64 ? (CPT == 8 ? 2 : CPT == 4 ? 3 : 4) : (CPT == 1 ? 3 : 2);
 
 template <int N>
 __device__ __forceinline__ void load_p(const float* src, float (&p)[N]) {
@@ -96,16 +96,24 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
     }
     const bool bad_block = cross_bad_block(a, p, kKeys, tid, kThreads);
     const int32_t* const table = a.block_tables + static_cast<size_t>(p.s) * a.max_blocks_per_seq;
+    // this thread's chunk of RPP rows of each block
+    constexpr int RPP = kThreads / CPR;
+    const int lc = tid % CPR, lr = tid / CPR;
+    const long long head = static_cast<long long>(p.kvh) * kBlockSize * D + lr * D + 4 * lc;
+    const long long block = static_cast<long long>(a.num_kv_heads) * kBlockSize * D;
     auto load = [&](float* dst, const void* cache, int t, bool swizzle) {
-      for (int i = tid; i < kKeys * CPR; i += kThreads) {
-        const int r = i / CPR, c = i % CPR;
-        const int key = t * kKeys + r;
-        const bool live = key < p.n;
-        int id = live ? __ldg(table + key / kBlockSize) : 0;
+      const float* const base = static_cast<const float*>(cache) + head;
+#pragma unroll
+      for (int b = 0; b < kKeys / kBlockSize; ++b) {
+        const int key = t * kKeys + b * kBlockSize;
+        int id = key < p.n ? __ldg(table + key / kBlockSize) : 0;
         if (id < 0 || id >= a.num_blocks) id = 0;  // (the piece is poisoned)
-        const float* row = static_cast<const float*>(cache) +
-                       ((static_cast<size_t>(id) * a.num_kv_heads + p.kvh) * kBlockSize + key % kBlockSize) * D;
-        cp_async16(smem_addr(dst + r * D + 4 * (c ^ (swizzle ? r & 7 : 0))), row + 4 * c, live);
+        const float* const src = base + id * block;
+#pragma unroll
+        for (int r = 0; r < kBlockSize; r += RPP) {
+          const int row = b * kBlockSize + r + lr;
+          cp_async16(smem_addr(dst + row * D + 4 * (lc ^ (swizzle ? row & 7 : 0))), src + r * D, key + r + lr < p.n);
+        }
       }
       cp_commit();
     };
