@@ -871,7 +871,7 @@ pa_status pa_cross_attention(void* out, const void* q, const void* k_cache, cons
   // a worker's share of the tiles is counted in 32 bits
   const long long groups =
       static_cast<long long>(num_query_tokens) * (num_q_heads / num_kv_heads) / k.cols + num_seqs;
-  if (groups * num_kv_heads >= (1LL << 36) / (len_cap / k.keys + 1)) return PA_ERR_UNSUPPORTED;
+  if (groups * num_kv_heads >= (1LL << 36) / (len_cap / k.keys + 32)) return PA_ERR_UNSUPPORTED;
   if (!workspace || workspace_bytes < p.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
 
   pa::CrossArgs a{};

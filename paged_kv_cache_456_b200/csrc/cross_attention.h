@@ -5,12 +5,14 @@
 // (query row, query head) pair of the KV head, column c of a sequence being
 // row c / G, head c % G.  An item's keys are cut into tiles; an item without
 // keys counts one tile (its rows are written as zeros).  All tiles are laid
-// end to end in (sequence, KV head, group, tile) order and cut into equal
-// contiguous shares, one per worker (a CTA), so every CTA gets the same number
-// of tiles however skewed the lengths are.  The run of one item's tiles inside
-// a share is a piece: a piece that is the whole item stores the output, any
-// other stores a partial state (m, l, o), and the CTA that stores the last of
-// an item's partials merges them, in the order of the keys:
+// end to end in (sequence, KV head, group, tile) order, `extra` units ahead of
+// each item's for what an item costs besides its tiles, and cut into equal
+// contiguous shares, one per worker (a CTA), so every CTA gets as much work
+// however skewed the lengths are.  (A cut inside the units ahead is one at the
+// item's first tile.)  The run of one item's tiles inside a share is a piece: a
+// piece that is the whole item stores the output, any other stores a partial
+// state (m, l, o), and the CTA that stores the last of an item's partials
+// merges them, in the order of the keys:
 //   M = max_j m_j,  out = sum_j 2^(m_j - M) o_j / sum_j 2^(m_j - M) l_j.
 // No CTA waits for another.  A worker has at most two partial pieces, hence
 // two slots: slot 2 w for the piece its share begins inside of, 2 w + 1 for
@@ -107,15 +109,15 @@ __device__ __forceinline__ int4 cross_seq(const CrossArgs& a, int s, int cols, i
   return make_int4(r0, r1 - r0, n, (((r1 - r0) << a.group_log2) + cols - 1) / cols);
 }
 
-// A worker's share: `left` tiles from tile `tile` of item `item` of sequence s
-// on; the first is tile `at` of all.
+// A worker's share: `left` units from unit `unit` of item `item` of sequence s
+// on; the first is unit `at` of all.
 struct CrossShare {
   long long at;
-  int left, s, item, tile;
+  int left, s, item, unit;
 };
 // (in shared memory: what the end of a piece needs)
 struct CrossTotal {
-  long long W;       // tiles of the call
+  long long W;       // units of the call
   int workers;       // workers that have some
   unsigned old[2];   // partials stored before this one, per column tile
   long long scratch[16];  // (a long long per warp, two more; at most 14 warps)
@@ -126,7 +128,7 @@ struct CrossTotal {
 // (a lane has up to four, whose lengths it loads together); more are spread
 // over the CTA.
 template <int THREADS>
-__device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, int keys, CrossTotal* total) {
+__device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, int keys, int extra, CrossTotal* total) {
   long long* const scratch = total->scratch;
   constexpr int WARPS = THREADS / 32, MINE = 4;
   const int tid = threadIdx.x, lane = tid & 31, S = a.num_seqs;
@@ -134,8 +136,8 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
   const int parts = by_warp ? 32 : THREADS, part = by_warp ? lane : tid;
   const int per = (S + parts - 1) / parts;
   const int s0 = min(S, part * per), s1 = min(S, s0 + per);
-  auto tiles_of = [&](const int4& m) -> long long {
-    return static_cast<long long>(a.num_kv_heads) * m.w * cross_tiles(m.z, keys);
+  auto units_of = [&](const int4& m) -> long long {
+    return static_cast<long long>(a.num_kv_heads) * m.w * (extra + cross_tiles(m.z, keys));
   };
   long long local = 0;
   int bits = 0;
@@ -145,13 +147,13 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
     for (int k = 0; k < MINE; ++k) {
       int bit = 0;
       mine[k] = s0 + k < s1 ? cross_seq(a, s0 + k, cols, &bit) : make_int4(0, 0, 0, 0);
-      local += tiles_of(mine[k]);
+      local += units_of(mine[k]);
       bits |= bit;
     }
   } else {
     for (int s = s0; s < s1; ++s) {
       int bit;
-      local += tiles_of(cross_seq(a, s, cols, &bit));
+      local += units_of(cross_seq(a, s, cols, &bit));
       bits |= bit;
     }
   }
@@ -191,20 +193,20 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
     total->W = W;
     total->workers = workers;
   }
-  // one part's sequences hold the first tile
+  // one part's sequences hold the first unit
   const bool owner = run <= x.at && x.at < run + local;
   long long off = x.at - run;
-  int fs = 0, fitem = 0, ftile = 0;
+  int fs = 0, fitem = 0, funit = 0;
   auto place = [&](int s, const int4& m) -> bool {
-    const long long t = tiles_of(m);
+    const long long t = units_of(m);
     if (off >= t) {
       off -= t;
       return false;
     }
-    const int nt = cross_tiles(m.z, keys);
+    const int nt = extra + cross_tiles(m.z, keys);
     fs = s;
     fitem = off < (1LL << 31) ? static_cast<int>(off) / nt : static_cast<int>(off / nt);
-    ftile = static_cast<int>(off - static_cast<long long>(fitem) * nt);
+    funit = static_cast<int>(off - static_cast<long long>(fitem) * nt);
     return true;
   };
   if (by_warp) {
@@ -216,7 +218,7 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
     const int src = who ? __ffs(who) - 1 : 0;
     x.s = __shfl_sync(0xffffffffu, fs, src);
     x.item = __shfl_sync(0xffffffffu, fitem, src);
-    x.tile = __shfl_sync(0xffffffffu, ftile, src);
+    x.unit = __shfl_sync(0xffffffffu, funit, src);
     __syncthreads();
   } else {
     int* const res = reinterpret_cast<int*>(scratch + WARPS);
@@ -227,12 +229,12 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
       }
       res[0] = fs;
       res[1] = fitem;
-      res[2] = ftile;
+      res[2] = funit;
     }
     __syncthreads();
     x.s = res[0];
     x.item = res[1];
-    x.tile = res[2];
+    x.unit = res[2];
   }
   return x;
 }
@@ -244,7 +246,7 @@ struct CrossPiece {
   int n, live;       // keys, live columns of the group
   int row;           // query row of column 0
   int slot;          // partial slot, or -1: the whole item
-  long long begin;   // the item's first tile
+  long long begin;   // the item's first tile, in units
   // column 0 of the group in q and out, in rows of D elements
   __device__ __forceinline__ long long base(const CrossArgs& a) const {
     return static_cast<long long>(row) * a.num_q_heads + (kvh << a.group_log2);
@@ -260,32 +262,37 @@ struct CrossWalk {
     int bit;
     m = x.left > 0 ? cross_seq(a, x.s, cols, &bit) : make_int4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ bool next(const CrossArgs& a, int cols, int keys, CrossPiece* p) {
-    if (x.left <= 0) return false;
-    while (x.item >= a.num_kv_heads * m.w) {
-      if (++x.s >= a.num_seqs) return false;
-      int bit;
-      m = cross_seq(a, x.s, cols, &bit);
-      x.item = x.tile = 0;
+  __device__ __forceinline__ bool next(const CrossArgs& a, int cols, int keys, int extra, CrossPiece* p) {
+    while (x.left > 0) {
+      if (x.item >= a.num_kv_heads * m.w) {
+        if (++x.s >= a.num_seqs) return false;
+        int bit;
+        m = cross_seq(a, x.s, cols, &bit);
+        x.item = x.unit = 0;
+        continue;
+      }
+      p->nt = cross_tiles(m.z, keys);
+      const int u0 = x.unit, u1 = min(extra + p->nt, u0 + x.left), item = x.item;
+      p->begin = x.at - u0 + extra;
+      x.at += u1 - u0;
+      x.left -= u1 - u0;
+      ++x.item;
+      x.unit = 0;
+      p->t0 = max(0, u0 - extra);
+      p->t1 = u1 - extra;
+      if (p->t1 <= p->t0) continue;  // (nothing but units ahead)
+      p->s = x.s;
+      p->kvh = item / m.w;
+      p->grp = item - p->kvh * m.w;
+      p->n = m.z;
+      const int c0 = p->grp * cols;
+      p->live = min(cols, (m.y << a.group_log2) - c0);
+      p->row = m.x + (c0 >> a.group_log2);
+      const int w = blockIdx.x;
+      p->slot = p->t0 > 0 ? 2 * w : p->t1 < p->nt ? 2 * w + 1 : -1;
+      return true;
     }
-    p->s = x.s;
-    p->kvh = x.item / m.w;
-    p->grp = x.item - p->kvh * m.w;
-    p->n = m.z;
-    const int c0 = p->grp * cols;
-    p->live = min(cols, (m.y << a.group_log2) - c0);
-    p->row = m.x + (c0 >> a.group_log2);
-    p->nt = cross_tiles(m.z, keys);
-    p->t0 = x.tile;
-    p->t1 = min(p->nt, x.tile + x.left);
-    const int w = blockIdx.x;
-    p->slot = x.tile > 0 ? 2 * w : p->t1 < p->nt ? 2 * w + 1 : -1;
-    p->begin = x.at - x.tile;
-    x.at += p->t1 - p->t0;
-    x.left -= p->t1 - p->t0;
-    ++x.item;
-    x.tile = 0;
-    return true;
+    return false;
   }
 };
 // the workers that hold the pieces of p's item: the first, and how many

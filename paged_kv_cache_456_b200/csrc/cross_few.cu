@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kKeys = kBlockSize;
+constexpr int kExtra = 16;  // what an item costs besides its blocks, in blocks of a warp (measured: 8 to 24 alike)
 constexpr float kGrow = 8.f;  // log2 growth of a maximum before O is rescaled
 
 template <int D>
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
     if (warp == 0) s_abort = 0;
     fence_barrier_init();
   }
-  const CrossShare share = cross_share<kThreads>(a, COLS, kKeys, &s_total);  // (synchronises the CTA)
+  const CrossShare share = cross_share<kThreads>(a, COLS, kKeys, kExtra, &s_total);  // (synchronises the CTA)
 
   // ---- this warp's loads: blocks t0 + warp, + 8, ... of every piece with keys
   CrossWalk ahead(a, share, COLS);
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
   };
   auto issue = [&]() {
     while (more && ib >= iend) {
-      more = ahead.next(a, COLS, kKeys, &ip);
+      more = ahead.next(a, COLS, kKeys, kExtra, &ip);
       if (more && ip.n > 0) {
         ib = ip.t0 + warp;
         iend = ip.t1;
@@ -128,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
   CrossPiece p;
   int taken = 0;
   bool ok = true;
-  while (ok && walk.next(a, COLS, kKeys, &p)) {
+  while (ok && walk.next(a, COLS, kKeys, kExtra, &p)) {
     if (p.n == 0) {
       for (int i = tid; i < p.live * (D / 8); i += kThreads)
         reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +

@@ -26,9 +26,8 @@
 // The softmax of a tile takes the last running maximum on trust: the first
 // half's weights are computed while the tile's own maximum is, and computed
 // again in the rare case that it exceeds the running one by 2^8 or more.
-// The output leaves through a staging area of the warp, so that stores touch
-// whole rows: one row per lane and instruction cost 2000 cycles a tile in the
-// load-store unit, and delayed what was queued behind.
+// The output leaves straight from registers, 32 bytes (a whole sector) a lane and
+// store; whole rows by way of a staging area took as long.
 // Tried and slower (4 x 4096 x 4096, 32 heads; this form 0.90 ms): S in two
 // buffers of 64 keys a tile, whose MMAs cost a third more operand traffic (0.96
 // to 1.25 ms); an MMA warp for each tile, whose softmaxes then fall into step
@@ -51,6 +50,7 @@ namespace pa {
 namespace {
 
 constexpr int kCols = 128, kTiles = 2, kKeys = 128;
+constexpr int kExtra = 1;  // what an item costs besides its tiles (16 ragged sequences: 0 74.7, 1 62.9, 2 63.4, 3 66.3 us)
 constexpr int kBlocks = kKeys / kBlockSize;  // blocks of a K/V tile
 constexpr int kWg = 128;                     // threads of a softmax warpgroup
 constexpr int kProducerWarp = 8, kMmaWarp = 9, kQWarp = 10, kThreads = 384;
@@ -67,8 +67,7 @@ struct Shape {
   static constexpr int KT = kKeys * D * 2;      // bytes of a K or V tile
   static constexpr int HALF = kKeys * 128;      // bytes of a 64-element half of it
   static constexpr int NS = D == 128 ? 4 : 8;   // ring slots
-  static constexpr int STAGE = 32 * 128;        // bytes of a softmax warp's staging area: 32 rows x 64 elements
-  static constexpr int SMEM = 1024 + kTiles * QT + NS * KT + 8 * STAGE + 256;
+  static constexpr int SMEM = 1024 + kTiles * QT + NS * KT + 256;
 };
 
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
@@ -166,7 +165,7 @@ struct WarpWalk {
     bool ok = false;
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
-      while ((ok = walk.next(a, kTiles * kCols, kKeys, &piece)) && with_keys && piece.n == 0) {
+      while ((ok = walk.next(a, kTiles * kCols, kKeys, kExtra, &piece)) && with_keys && piece.n == 0) {
       }
     ok = __any_sync(0xffffffffu, ok);
     __syncwarp();
@@ -193,8 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
   unsigned char* const sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
   unsigned char* const sQ = sm;                  // [kTiles][QT]
   unsigned char* const sR = sQ + kTiles * QT;    // [NS][KT]: K and V tiles in turn
-  unsigned char* const sO = sR + NS * KT;        // [8 warps][STAGE]
-  const uint32_t b0 = smem_addr(sO + 8 * C::STAGE);
+  const uint32_t b0 = smem_addr(sR + NS * KT);
   // barriers: full[NS] empty[NS] | per tile: sfull, p[2], odone, qfull, qempty, sync | drain
   auto FULL = [&](int i) { return b0 + 8 * i; };
   auto EMPTY = [&](int i) { return b0 + 8 * (NS + i); };
@@ -234,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
   }
   tc::fence_before_sync();
   {
-    const CrossShare share = cross_share<kThreads>(a, kTiles * kCols, kKeys, &s_total);  // (synchronises the CTA)
+    const CrossShare share = cross_share<kThreads>(a, kTiles * kCols, kKeys, kExtra, &s_total);  // (synchronises the CTA)
     if (lane == 0) s_walk[warp].walk = CrossWalk(a, share, kTiles * kCols);
     __syncwarp();
   }
@@ -425,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     const int t = warp / 4, col = tid % kWg;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16);
     const uint32_t s_addr = lane_base + t * kKeys, o_addr = lane_base + kTiles * kKeys + t * 128;
-    unsigned char* const stage = sO + warp * C::STAGE;
+    const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     int step = 0, sn = 0, on = 0, syncs = 0;
     bool ok = true;
     auto group_sync = [&]() -> bool {  // the 128 threads of this warpgroup
@@ -436,31 +434,17 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     // with the rounded product; another scale is applied to the scores one by one.
     const float mul = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;
     while (ok && walk.next(a, false)) {
-      // rows of this warp's columns at `base`, 64 elements of each row, from
-      // the staging area (chunk i of row r at i ^ (r % 8)) or zeros
-      auto put_rows = [&](const CrossPiece& p, int base, bool zeros) {
-        const int i = lane % 8;
-        __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.out) + p.base(a) * D + base + 8 * i;
-        const int c0 = t * kCols + (warp % 4) * 32 + lane / 8;
-        uint4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = 4 * k + lane / 8;
-          v[k] = *reinterpret_cast<const uint4*>(stage + r * 128 + ((i ^ (r & 7)) << 4));
-          if (zeros) v[k] = make_uint4(0, 0, 0, 0);
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (c0 + 4 * k < p.live) *reinterpret_cast<uint4*>(dst + cross_column(a, c0 + 4 * k) * D) = v[k];
-      };
       int left, tiles;  // keys from this tile on, tiles to go
       bool bad;
       {
         const CrossPiece p = walk.get();
         const bool mine = t < live_tiles(p);
         if (p.n == 0) {
-          if (mine)
-            for (int h = 0; h < KB; ++h) put_rows(p, 64 * h, true);
+          if (mine && t * kCols + col < p.live) {
+            uint4* const dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
+                                                        (p.base(a) + cross_column(a, t * kCols + col)) * D);
+            for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+          }
           continue;
         }
         tiles = p.t1 - p.t0;
@@ -608,65 +592,70 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         }
       }
       const float inv = 1.f / L;
+      const bool live = t * kCols + col < p.live;
+      __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.out) +
+                                 (p.base(a) + (live ? cross_column(a, t * kCols + col) : 0)) * D;
+      // (every lane runs the warp-wide TMEM loads; only live columns are stored)
 #pragma unroll 1
-      for (int h = 0; h < KB; ++h) {
-        __syncwarp();  // (the staging area has been read)
-#pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          uint32_t o[32];
-          tc::tmem_ld32(o_addr + 64 * h + 32 * q, o);
-          tc::tmem_wait_ld(o);
-          const int at = ((8 * h + 4 * q) * kCols + col) * 8;  // these dims in a partial
-          if (store) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float v[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * i + e]);
-              cross_store8(a.part_o + pt * kCols * D + at + i * kCols * 8, v);
-            }
-            continue;
-          }
-          if (pieces > 1) {
-            float acc[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-            for (int x = 0; x < pieces; ++x) {
-              if (first + x == blockIdx.x) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) acc[k] = fmaf(wgt, __uint_as_float(o[k]), acc[k]);
-                continue;
-              }
-              const size_t xt = cross_tile<kTiles>(first, x, t);
-              const float wx = cross_weight(__ldcg(a.part_ml + xt * kCols + col).x, M);
-              float4 v[8];
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                v[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + xt * kCols * D + at + i / 2 * kCols * 8) + i % 2);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                acc[4 * i] = fmaf(wx, v[i].x, acc[4 * i]);
-                acc[4 * i + 1] = fmaf(wx, v[i].y, acc[4 * i + 1]);
-                acc[4 * i + 2] = fmaf(wx, v[i].z, acc[4 * i + 2]);
-                acc[4 * i + 3] = fmaf(wx, v[i].w, acc[4 * i + 3]);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(acc[k]);
-          }
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tc::tmem_ld32(o_addr + 32 * q, o);
+        tc::tmem_wait_ld(o);
+        const int at = (4 * q * kCols + col) * 8;  // these dims in a partial
+        if (store) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t v[4];
+            float v[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = pack_bf16(__uint_as_float(o[8 * i + 2 * e]) * inv, __uint_as_float(o[8 * i + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + i) ^ (lane & 7)) << 4)) =
-                make_uint4(v[0], v[1], v[2], v[3]);
+            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * i + e]);
+            cross_store8(a.part_o + pt * kCols * D + at + i * kCols * 8, v);
           }
+          continue;
         }
-        if (!store) {
-          __syncwarp();
-          put_rows(p, 64 * h, zero);
+        if (pieces > 1) {
+          float acc[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+          for (int x = 0; x < pieces; ++x) {
+            if (first + x == blockIdx.x) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) acc[k] = fmaf(wgt, __uint_as_float(o[k]), acc[k]);
+              continue;
+            }
+            const size_t xt = cross_tile<kTiles>(first, x, t);
+            const float wx = cross_weight(__ldcg(a.part_ml + xt * kCols + col).x, M);
+            float4 v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              v[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + xt * kCols * D + at + i / 2 * kCols * 8) + i % 2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[4 * i] = fmaf(wx, v[i].x, acc[4 * i]);
+              acc[4 * i + 1] = fmaf(wx, v[i].y, acc[4 * i + 1]);
+              acc[4 * i + 2] = fmaf(wx, v[i].z, acc[4 * i + 2]);
+              acc[4 * i + 3] = fmaf(wx, v[i].w, acc[4 * i + 3]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(acc[k]);
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // 16 dims (32 bytes) at a time
+          uint32_t v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = zero ? 0u
+                        : pack_bf16(__uint_as_float(o[16 * i + 2 * e]) * inv, __uint_as_float(o[16 * i + 2 * e + 1]) * inv);
+          uint4* const to = reinterpret_cast<uint4*>(dst + 32 * q + 16 * i);
+          if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(v[0]), "r"(v[1]),
+                         "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                         : "memory");
+          } else {
+            to[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            to[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          }
         }
       }
       tc::fence_before_sync();  // (O has been read before this warpgroup's next P lets it be written)
