@@ -368,12 +368,14 @@ pa_status pa_prefill(void *out, const void *q, const void *k_cache, const void *
  * pa_reshape_and_cache (or pa_rope_append), and read by every later step:
  * one row per sequence while generating, many rows for a prompt or an image.
  *
- *   q, out          device, [num_query_tokens][num_q_heads][head_dim].
+ *   q, out          device, [num_query_tokens][num_q_heads][head_dim]; out
+ *                   must not overlap q.
  *   query_start     device int32 [num_seqs + 1], non-decreasing, values in
  *                   [0, num_query_tokens].  Rows before query_start[0] and
  *                   from query_start[num_seqs] on are not touched.  A
  *                   sequence whose pair is out of order or out of range sets
- *                   PA_ERRBIT_QUERY; its rows may be left unwritten.
+ *                   PA_ERRBIT_QUERY; its rows may be left unwritten, and rows
+ *                   that two pairs cover then hold either's result.
  *   context_lens    a length outside [0, min(max_context_len,
  *                   max_blocks_per_seq * 16)] sets PA_ERRBIT_CONTEXT_LEN, a
  *                   block id outside the cache among the blocks attended to
@@ -384,11 +386,18 @@ pa_status pa_prefill(void *out, const void *q, const void *k_cache, const void *
  *                   (pa_decode_workspace_init); every call leaves it ready
  *                   for the next, of whatever sizes.  Two calls that may run
  *                   at the same time must not share one.
- *   Everything else, and the supported shapes, are as in pa_decode.
+ *   Everything else, and the supported shapes, are as in pa_decode, but that
+ *   num_q_heads <= 32768, num_query_tokens * num_q_heads < 2^31 and contexts
+ *   are of at most 2^30 tokens (PA_ERR_UNSUPPORTED above).
  *
- * fp32 caches: fp32 arithmetic throughout.  The work is cut into equal
- * shares whatever the lengths, a split row's parts being merged exactly (up
- * to rounding); repeated calls give the same bits.
+ * One launch.  Its work is cut into equal shares whatever the lengths, a split
+ * row's parts being merged exactly (up to rounding); repeated calls give the
+ * same bits.  fp32 caches: fp32 arithmetic throughout, on the CUDA cores.  bf16:
+ * the tensor cores, fp32 accumulation; a softmax weight is rounded to bf16 for
+ * its product with V, the sum of the weights is taken before that rounding.  Up
+ * to 32 (row, query head) columns per KV head and sequence, on average, K and V
+ * are streamed past them once (one row a sequence while generating); more take
+ * the tcgen05 tensor cores, 256 columns at a time.
  */
 pa_status pa_cross_attention_workspace_size(int num_seqs, int num_query_tokens, int num_q_heads,
                                             int num_kv_heads, int head_dim, int max_context_len,

@@ -4,7 +4,9 @@ The compute path is the C-ABI library ``libpa.so`` (hand-written CUDA,
 declared in ``include/paged_attention.h``); ``ops`` is its thin Python
 binding: ``decode``, ``decode_append`` (slot write fused into decode),
 ``decode_noalloc``, ``prefill`` (several query tokens per sequence),
-``reshape_and_cache`` and ``copy_blocks``.  ``block_allocator`` and
+``cross_attention`` (rows that attend to all of a sequence's tokens),
+``reshape_and_cache``, ``rope_append`` (the same with rotary positions applied
+on the way, and to the queries) and ``copy_blocks``.  ``block_allocator`` and
 ``workloads`` build seeded inputs on the host, ``capacity`` restates the
 pages' capacity arithmetic, and ``scheduler`` simulates the
 continuous-batching loop that drives the GPU path step by step.

@@ -184,6 +184,46 @@ def test_scores_that_grow_along_the_keys(dtype, rows):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 3, 20, 40, 200, 300])
+def test_one_item_over_every_worker(dtype, rows):
+    """One KV head's keys cut into as many pieces as there are workers, of one sequence or beside short ones."""
+    for keys in ((40000,), (3, 30001, 17)):
+        c = Case((rows,) * len(keys), keys, dtype=dtype, hkv=1, G=1, D=64)
+        ws = c.workspace()
+        for _ in range(2):
+            out, err = c.call(ws=ws)
+            assert err == 0
+            c.check(out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [(1, 2, 1), (90, 300, 2)])
+def test_infinite_scores(dtype, rows):
+    """Keys whose scores are -inf weigh nothing; rows that see nothing else are NaN, as the softmax is."""
+    c = Case(rows, (300, 700, 40), dtype=dtype, hkv=1, G=2, D=64)
+    c.q[:] = c.q.abs() + 0.1
+    pos = torch.arange(0, 700, 3, device="cuda")
+    c.k[c.tables[1].long()[pos // BLOCK], 0, pos % BLOCK, 5] = -math.inf
+    pos = torch.arange(40, device="cuda")
+    c.k[c.tables[2].long()[pos // BLOCK], 0, pos % BLOCK, 5] = -math.inf
+    out, err = c.call()
+    assert err == 0
+    assert out[c.starts[2]:c.starts[3]].isnan().all()
+    c.check(out, skip=(1, 2))
+    ids = c.tables[1, :44].long()
+    k, v = (x[ids, 0].reshape(-1, 64)[:700].double() for x in (c.k, c.v))
+    seen = torch.ones(700, dtype=torch.bool, device="cuda")
+    seen[::3] = False
+    q = c.q[c.starts[1]:c.starts[2]].double()
+    p = torch.softmax(c.scale * (q @ k[seen].t()), dim=-1)
+    want, a = p @ v[seen], p @ v[seen].abs()
+    x = c.scale * (q.abs() @ k[seen].abs().t()).amax(-1, keepdim=True)
+    half = torch.finfo(c.dt).eps / 2
+    tol = (2 * (2 * 68 * U * x + 4 * U) + 4 * 764 * U + (half if dtype == "bf16" else 0)) * a
+    assert ((out[c.starts[1]:c.starts[2]].double() - want).abs() <= tol + half * (want.abs() + tol)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_batch_of_many_sequences(dtype):
     """More sequences than the plan keeps on chip, one row or none each, most of them without keys or short."""
     g = torch.Generator().manual_seed(5)
