@@ -49,7 +49,7 @@ typedef enum pa_status {
     PA_OK = 0,
     PA_ERR_INVALID_ARG = 1,  /* a null pointer, a negative size, a misaligned buffer ... */
     PA_ERR_UNSUPPORTED = 2,  /* a valid shape the library has no kernel for            */
-    PA_ERR_WORKSPACE = 3,    /* the decode workspace is missing or too small            */
+    PA_ERR_WORKSPACE = 3,    /* the workspace is missing or too small                   */
     PA_ERR_CUDA = 4          /* the CUDA runtime refused a query or a launch            */
 } pa_status;
 
@@ -66,10 +66,10 @@ typedef enum pa_dtype {
 #define PA_ERRBIT_SLOT        4   /* slot_mapping[t] >= num_blocks * block_size: skipped    */
 #define PA_ERRBIT_PAIR        8   /* a copy pair with an id outside [0, num_blocks) or
                                      src == dst: skipped                                  */
-#define PA_ERRBIT_TIMEOUT     16  /* a bounded device wait ran out; results are invalid and
-                                     the decode workspace must be re-initialised           */
-#define PA_ERRBIT_QUERY       32  /* pa_prefill: a sequence's query_start pair out of order
-                                     or more query rows than tokens: its rows written as 0 */
+#define PA_ERRBIT_TIMEOUT     16  /* a bounded device wait ran out; results are invalid, and
+                                     a workspace the call used must be initialised again   */
+#define PA_ERRBIT_QUERY       32  /* pa_prefill, pa_cross_attention: a query_start pair out
+                                     of order; pa_prefill: more rows than tokens (rows 0)   */
 #define PA_ERRBIT_GROUP       64  /* pa_decode_shared_prefix: a group entry that does not
                                      match the block tables (or a sequence two groups list)
                                      was ignored; those sequences were attended in full, so
@@ -258,6 +258,27 @@ pa_status pa_rope_append(void *q_out, const void *q, const void *key, const void
                          int block_size, int num_blocks, pa_dtype dtype, int32_t *err_flag,
                          void *stream);
 
+/* The same call with its arguments in one struct, for language bindings that
+ * pay for every argument; NULL is PA_ERR_INVALID_ARG. */
+typedef struct pa_rope_append_args {
+    void *q_out;
+    const void *q, *key, *value;
+    void *k_cache, *v_cache;
+    const int64_t *slot_mapping, *positions;
+    const float *inv_freq;
+    const int32_t *pair_axis;
+    int64_t q_out_stride, q_stride, key_stride, value_stride;
+    int32_t *err_flag;
+    int num_axes, rotary_dim;
+    pa_rope_style style;
+    float rot_scale;
+    int num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks;
+    pa_dtype dtype;
+    void *stream;
+} pa_rope_append_args;
+
+pa_status pa_rope_append_packed(const pa_rope_append_args *args);
+
 /* ------------------------------------------------------------------------
  * Fused slot write + decode attention
  * ------------------------------------------------------------------------
@@ -410,6 +431,23 @@ pa_status pa_cross_attention(void *out, const void *q, const void *k_cache, cons
                              int max_blocks_per_seq, int num_blocks, int max_context_len,
                              float scale, pa_dtype dtype, void *workspace, size_t workspace_bytes,
                              int32_t *err_flag, void *stream);
+
+/* The same call with its arguments in one struct, as pa_rope_append_packed. */
+typedef struct pa_cross_attention_args {
+    void *out;
+    const void *q, *k_cache, *v_cache;
+    const int32_t *block_tables, *context_lens, *query_start;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t *err_flag;
+    int num_seqs, num_query_tokens, num_q_heads, num_kv_heads, head_dim, block_size;
+    int max_blocks_per_seq, num_blocks, max_context_len;
+    float scale;
+    pa_dtype dtype;
+    void *stream;
+} pa_cross_attention_args;
+
+pa_status pa_cross_attention_packed(const pa_cross_attention_args *args);
 
 /* ------------------------------------------------------------------------
  * Prefix-deduplicated decode

@@ -909,6 +909,25 @@ pa_status pa_cross_attention(void* out, const void* q, const void* k_cache, cons
   return PA_OK;
 }
 
+pa_status pa_rope_append_packed(const pa_rope_append_args* x) {
+  if (!x) return PA_ERR_INVALID_ARG;
+  return pa_rope_append(x->q_out, x->q, x->key, x->value, x->k_cache, x->v_cache, x->slot_mapping,
+                        x->positions, x->inv_freq, x->pair_axis, x->num_axes, x->rotary_dim,
+                        x->style, x->rot_scale, x->q_out_stride, x->q_stride, x->key_stride,
+                        x->value_stride, x->num_tokens, x->num_q_heads, x->num_kv_heads,
+                        x->head_dim, x->block_size, x->num_blocks, x->dtype, x->err_flag,
+                        x->stream);
+}
+
+pa_status pa_cross_attention_packed(const pa_cross_attention_args* x) {
+  if (!x) return PA_ERR_INVALID_ARG;
+  return pa_cross_attention(x->out, x->q, x->k_cache, x->v_cache, x->block_tables,
+                            x->context_lens, x->query_start, x->num_seqs, x->num_query_tokens,
+                            x->num_q_heads, x->num_kv_heads, x->head_dim, x->block_size,
+                            x->max_blocks_per_seq, x->num_blocks, x->max_context_len, x->scale,
+                            x->dtype, x->workspace, x->workspace_bytes, x->err_flag, x->stream);
+}
+
 pa_status pa_copy_blocks(void* k_cache, void* v_cache, const int32_t* block_mapping,
                          int num_pairs, int num_kv_heads, int head_dim, int block_size,
                          int num_blocks, pa_dtype dtype, int32_t* err_flag, void* stream) {

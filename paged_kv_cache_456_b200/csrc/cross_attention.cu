@@ -6,6 +6,7 @@
 //   x_i = scale q[r][h] . K_i,   i = 0 .. n - 1.
 #include "cross_attention.h"
 
+#include <exception>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -45,7 +46,7 @@ cudaError_t launch_cross_attention(CrossArgs& a, const CrossKernel& k, int num_s
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  {
+  try {
     std::lock_guard<std::mutex> lock(g_mu);
     bool& ready = g_ready[std::make_pair(dev, k.fn)];
     if (!ready) {
@@ -54,6 +55,8 @@ cudaError_t launch_cross_attention(CrossArgs& a, const CrossKernel& k, int num_s
         return e;
       ready = true;
     }
+  } catch (const std::exception&) {  // (the map's memory, the lock: nothing passes a C entry)
+    return cudaErrorMemoryAllocation;
   }
   void* params[] = {&a};
   return cudaLaunchKernel(k.fn, dim3(num_sms * k.ctas_per_sm), dim3(k.threads), params, k.smem, stream);

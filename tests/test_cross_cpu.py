@@ -1,6 +1,10 @@
 """pa_cross_attention's refusals, on a machine without a GPU: bad arguments return a status before any CUDA call, and
 the binding refuses tensors that the library cannot take."""
 import ctypes
+import os
+import re
+import struct
+import subprocess
 
 import pytest
 import torch
@@ -63,3 +67,31 @@ def test_the_binding_refuses_host_tensors():
     with pytest.raises(ValueError, match="CUDA"):
         ops.cross_attention(q, q, c, c, i[:, None], i, torch.zeros(3, dtype=torch.int32), scale=1.0, max_context_len=16,
                             workspace=torch.zeros(64, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("args", [dict(T=0), dict(S=-1), dict(Hq=7), dict(D=32), dict(bs=32), dict(N=1 << 27), dict(dt=7),
+                                  dict(scale=float("nan")), dict(max_len=-1), dict(qs=None), dict(out=24), dict(B=0)])
+def test_the_packed_call_is_the_same_call(lib, args):
+    a = dict(out=16, q=16, kc=16, vc=16, tables=16, lens=16, qs=16, ws=16, bytes=1 << 20, err=0, S=3, T=9, Hq=8, Hkv=2, D=64,
+             bs=16, B=10, N=40, max_len=100, scale=0.125, dt=ops.PA_BF16, stream=0)
+    a.update(args)
+    fields = "out q kc vc tables lens qs ws bytes err S T Hq Hkv D bs B N max_len scale dt stream".split()
+    assert lib.pa_cross_attention_packed(ops._CROSS_ARGS.pack(*(a[f] or 0 for f in fields))) == call(lib, **args)
+    assert lib.pa_cross_attention_packed(None) == ops.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name,layout", [("pa_rope_append_args", ops._ROPE_ARGS), ("pa_cross_attention_args", ops._CROSS_ARGS)])
+def test_the_struct_is_laid_out_as_in_c(tmp_path, name, layout):
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    fields = re.search(r"typedef struct " + name + r" \{(.*?)\}", open(os.path.join(header, "paged_attention.h")).read(), re.S)[1]
+    fields = re.findall(r"(\w+)\s*[,;]", fields)
+    src = (f'#include <stdio.h>\n#include "paged_attention.h"\n#define P(f) '
+           f'printf("%zu %zu\\n", offsetof({name}, f), sizeof((({name}*)0)->f))\n'
+           f'int main(void) {{ {"".join(f"P({f});" for f in fields)} return 0; }}\n')
+    exe = str(tmp_path / "offsets")
+    subprocess.run(["gcc", "-std=c99", "-I", header, "-x", "c", "-", "-o", exe], input=src, text=True, check=True)
+    c = [tuple(map(int, line.split())) for line in subprocess.run([exe], capture_output=True, text=True, check=True).stdout.splitlines()]
+    codes = [ch for n, ch in re.findall(r"(\d*)([A-Za-z])", layout.format) for _ in range(int(n or 1))]
+    assert len(codes) == len(c) == len(fields)
+    for i, (ch, (offset, size)) in enumerate(zip(codes, c)):
+        assert struct.calcsize("".join(codes[:i + 1])) == offset + size and struct.calcsize(ch) == size, fields[i]

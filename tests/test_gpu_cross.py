@@ -373,6 +373,49 @@ def test_the_binding_refuses_on_the_device():
         c.call(ws=ws[8:])
 
 
+def wrong(t):
+    """The tensor as the binding must not take it: on the host, of another type, shape or layout."""
+    other = {torch.bfloat16: torch.float32, torch.float32: torch.float64, torch.int32: torch.int64,
+             torch.int64: torch.int32, torch.uint8: torch.uint8}[t.dtype]
+    yield t.cpu()
+    if other is not t.dtype:
+        yield t.to(other)
+        yield t[None]
+        yield t[:0] if t.shape[0] else t
+    yield torch.stack((t, t), dim=-1)[..., 0] if t.numel() > 1 else t.cpu()
+
+
+@pytest.mark.parametrize("name", ["out", "q", "k", "v", "tables", "lens", "qs", "ws", "err"])
+def test_the_binding_refuses_each_tensor(name):
+    c = Case((4, 2), (40, 50), G=2, D=64)
+    good = dict(out=torch.empty_like(c.q), q=c.q, k=c.k, v=c.v, tables=c.tables, lens=c.lens, qs=c.qs, ws=c.workspace(),
+                err=torch.zeros(1, dtype=torch.int32, device="cuda"))
+    for bad in wrong(good[name]):
+        if name == "err" and bad.is_cuda and bad.dtype is torch.int32 and bad.numel():
+            continue  # (an error word of any shape will do)
+        x = dict(good, **{name: bad})
+        with pytest.raises((ValueError, TypeError)):
+            ops.cross_attention(x["out"], x["q"], x["k"], x["v"], x["tables"], x["lens"], x["qs"], scale=1.0,
+                                max_context_len=50, workspace=x["ws"], err_flag=x["err"])
+
+
+@pytest.mark.parametrize("name", ["q_out", "q", "key", "value", "k", "v", "slots", "pos", "freq", "axis", "err"])
+def test_the_rotary_binding_refuses_each_tensor(name):
+    T, dev = 6, "cuda"
+    r = lambda *s: torch.randn(*s, device=dev).bfloat16()  # noqa: E731
+    good = dict(q_out=r(T, 4, 64), q=r(T, 4, 64), key=r(T, 2, 64), value=r(T, 2, 64), k=r(3, 2, 16, 64), v=r(3, 2, 16, 64),
+                slots=torch.arange(T, device=dev), pos=torch.arange(2 * T, device=dev).view(2, T),
+                freq=torch.ones(32, device=dev), axis=torch.zeros(32, dtype=torch.int32, device=dev),
+                err=torch.zeros(1, dtype=torch.int32, device=dev))
+    for bad in wrong(good[name]):
+        if name == "err" and bad.is_cuda and bad.dtype is torch.int32 and bad.numel():
+            continue
+        x = dict(good, **{name: bad})
+        with pytest.raises((ValueError, TypeError, ops.PagedAttentionError)):
+            ops.rope_append(x["q_out"], x["q"], x["key"], x["value"], x["k"], x["v"], x["slots"], x["pos"], x["freq"],
+                            pair_axis=x["axis"], err_flag=x["err"])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_run_of_the_operators_together(dtype):
     """Encoder states written once with their rotary positions, then prompts of several rows and generated rows that

@@ -80,3 +80,25 @@ def test_rows_may_lie_apart():
     assert ops._rows_ptr("t", t, (3, 4, 64), torch.float32) == (t.data_ptr(), 400)
     with pytest.raises(ValueError):
         ops._array_ptr("a", torch.zeros(4, 6)[:, :3], (4, 3), torch.float32)
+
+
+FIELDS = "q_out q key value kc vc slots pos freq axis os qs ks vs err axes rot style rot_scale T Hq Hkv D bs N dt stream".split()
+
+
+@pytest.mark.parametrize("args", [dict(T=0), dict(axes=9), dict(rot=24), dict(rot_scale=float("nan")), dict(bs=0),
+                                  dict(ks=64), dict(vs=0), dict(dt=5), dict(pos=None), dict(Hq=1 << 16, qs=1 << 22, os=1 << 22)])
+def test_the_packed_call_is_the_same_call(lib, args):
+    a = dict(q_out=16, q=16, key=16, value=16, kc=16, vc=16, slots=16, pos=16, freq=16, axis=None, axes=1, rot=64, style=0,
+             rot_scale=1.0, os=512, qs=512, ks=128, vs=128, T=4, Hq=8, Hkv=2, D=64, bs=16, N=10, dt=ops.PA_BF16, err=None,
+             stream=None)
+    a.update(args)
+    want = call(lib, **args)
+    assert lib.pa_rope_append_packed(ops._ROPE_ARGS.pack(*(a[f] or 0 for f in FIELDS))) == want
+    assert lib.pa_rope_append_packed(None) == ops.PA_ERR_INVALID_ARG
+
+
+def test_an_argument_out_of_its_range_is_refused(lib):
+    for bad in (dict(T=1 << 31), dict(D=-(1 << 31) - 1), dict(ks=1 << 63)):
+        a = dict.fromkeys(FIELDS, 0) | bad
+        with pytest.raises(ValueError, match="range"):
+            ops._call_on(0, lib.pa_rope_append_packed, "pa_rope_append", 0, ops._ROPE_ARGS, *(a[f] for f in FIELDS[:-1]))
