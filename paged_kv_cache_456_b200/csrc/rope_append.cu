@@ -21,7 +21,7 @@
 // Two kernels.  Where a row's units divide a warp (every power-of-two head_dim
 // up to 512 bf16 or 256 fp32 elements, with any rotary_dim that leaves whole
 // units), a warp takes a token, or a slice of its rows: a lane keeps the same
-// place in every row, its angles in registers, and three rows in flight; no
+// place in every row, its angles in registers, and three or four rows in flight; no
 // division, no barrier.  Other shapes take a CTA per few tokens, its units laid
 // end to end, angles read from shared memory per unit.  Measured on what both
 // can do, 16384 tokens of 48 rows of 256 bytes (402 MB): 67 us (91 %
@@ -227,12 +227,13 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeArgs a)
 // A warp per (token, slice of its rows); UPR = units of a row, a divisor of 32.
 // ---------------------------------------------------------------------------
 constexpr int kWarps = 2;      // per CTA
-constexpr int kRowsAhead = 3;  // rows a lane has in flight
 constexpr int kMaxHalf = 256;  // rotated pairs, at most
 constexpr long long kL2Bytes = 126LL << 20;
 constexpr int kWarpsWanted = 12;  // warps an SM, before a token's rows are cut
+constexpr int kTokensAtOnce = 16;  // tokens an SM up to which no warp waits for another's place
 
-template <typename T, bool ADJACENT, bool STREAM>
+// AHEAD: the rows that a lane has in flight.
+template <typename T, bool ADJACENT, bool STREAM, int AHEAD>
 __global__ void __launch_bounds__(kWarps * 32) rope_append_warp_kernel(const RopeArgs a, int upr, int slices) {
   constexpr int VE = 16 / sizeof(T);
   extern __shared__ float smem[];
@@ -297,11 +298,11 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_warp_kernel(const Rop
     r.dst = reinterpret_cast<uint4*>(dst);
     return r;
   };
-  Row row[kRowsAhead];
-  Chunk<T> x0[kRowsAhead], x1[kRowsAhead];
+  Row row[AHEAD];
+  Chunk<T> x0[AHEAD], x1[AHEAD];
   auto load = [&](int it) {
 #pragma unroll
-    for (int k = 0; k < kRowsAhead; ++k) {
+    for (int k = 0; k < AHEAD; ++k) {
       row[k] = locate(it + k);
       if (row[k].src) {
         x0[k].v = STREAM ? __ldcs(row[k].src + row[k].c0) : row[k].src[row[k].c0];
@@ -328,10 +329,10 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_warp_kernel(const Rop
       s[j] = s_sin[p];
     }
   }
-  for (int it = it0; it < it1; it += kRowsAhead) {
+  for (int it = it0; it < it1; it += AHEAD) {
     if (it != it0) load(it);
 #pragma unroll
-    for (int k = 0; k < kRowsAhead; ++k) {
+    for (int k = 0; k < AHEAD; ++k) {
       if (!row[k].src) continue;
       if (row[k].turn) {
 #pragma unroll
@@ -385,10 +386,20 @@ cudaError_t launch_rope_append(RopeArgs a, int elem_bytes, bool adjacent, int nu
       auto go = [&](auto kernel) {
         kernel<<<static_cast<unsigned>(ctas), kWarps * 32, smem, stream>>>(a, upr, static_cast<int>(slices));
       };
+      // Tokens that all have a place at once gain from a fourth row in flight (2048
+      // tokens of 80 rows: 16.9 us, 18.1 with three; 1024 of 48: 6.1, 6.4), more lose
+      // by the registers it takes (8192 of 20: 17.9, 15.3 with three).
+      const bool few = a.num_tokens <= static_cast<long long>(num_sms) * kTokensAtOnce;
       auto pick = [&](auto elem, auto stream_tag) {
         using T = decltype(elem);
         constexpr bool S = decltype(stream_tag)::value;
-        adjacent ? go(rope_append_warp_kernel<T, true, S>) : go(rope_append_warp_kernel<T, false, S>);
+        if constexpr (!S) {
+          if (few) {
+            adjacent ? go(rope_append_warp_kernel<T, true, S, 4>) : go(rope_append_warp_kernel<T, false, S, 4>);
+            return;
+          }
+        }
+        adjacent ? go(rope_append_warp_kernel<T, true, S, 3>) : go(rope_append_warp_kernel<T, false, S, 3>);
       };
       // More than the L2 holds (126 MB): read and written under the streaming
       // policy (402 MB: 67 us, 70 without); less may be read again from it (84 MB
