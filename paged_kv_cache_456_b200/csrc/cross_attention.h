@@ -54,7 +54,7 @@ struct CrossArgs {
   unsigned* count;             // [workers][column tiles]: partials stored of the item that begins
                                // in the worker and goes on; zero between calls
   float2* part_ml;             // [slots][columns]: running max (log2 units), sum of weights (< 0: poisoned)
-  float* part_o;               // [slots][column tiles][D / 8][columns of a tile][8]
+  float* part_o;               // [slots][column tiles][D / 8][columns of a tile][8] (cross_tc.cu: 4 dims for 8)
   CUtensorMap tm_k;            // bf16: caches as [num_blocks * Hkv * 16][D], boxes 16 x 64, SW128
   CUtensorMap tm_v;
   CUtensorMap tm_q;            // (where the kernel asks) q as (D, query heads, rows), boxes 64 x G x 128 / G
@@ -351,6 +351,13 @@ template <int TILES>
 __device__ __forceinline__ size_t cross_tile(int first, int i, int t) {
   return static_cast<size_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * TILES + t;
 }
+// Dims 4 ch to 4 ch + 3 of column c in a partial of COLS columns: CHUNK dims of a
+// column lie together, as many as a lane of the kernel stores at a time (so that
+// a warp's stores fill whole 32-byte sectors).
+template <int COLS, int CHUNK>
+__device__ __forceinline__ int cross_chunk(int ch, int c) {
+  return CHUNK == 4 ? (ch * COLS + c) * 4 : (ch / 2 * COLS + c) * 8 + (ch & 1) * 4;
+}
 // a piece's weight under the item's maximum (a piece that saw nothing finite
 // carries zeros, or the NaN that its scores make)
 __device__ __forceinline__ float cross_weight(float m, float M) { return m == -INFINITY ? 1.f : exp2f(m - M); }
@@ -358,7 +365,7 @@ __device__ __forceinline__ float cross_weight(float m, float M) { return m == -I
 // The merge of an item's column tile t (of TILES, COLS columns each) by
 // `team` threads, once all its partials are stored and visible.  A thread
 // takes 4 dims of a column at a time, UNITS of them and AHEAD pieces in flight.
-template <typename T, int D, int COLS, int TILES, int UNITS, int AHEAD>
+template <typename T, int D, int COLS, int TILES, int UNITS, int AHEAD, int CHUNK = 8>
 __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece& p, int first, int pieces, int t,
                                             int i0, int team) {
   const int live = min(COLS, p.live - t * COLS);
@@ -372,7 +379,7 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
     if (j < pieces) {
       const size_t pt = cross_tile<TILES>(first, j, t);
       ml = __ldcg(a.part_ml + pt * COLS + c);
-      o = __ldcg(reinterpret_cast<const float4*>(a.part_o + pt * COLS * D + (ch / 2 * COLS + c) * 8 + (ch & 1) * 4));
+      o = __ldcg(reinterpret_cast<const float4*>(a.part_o + pt * COLS * D + cross_chunk<COLS, CHUNK>(ch, c)));
     }
     float M = ml.x;
 #pragma unroll
@@ -429,7 +436,7 @@ __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece
         for (int u = 0; u < UNITS; ++u) {
           ml[j][u] = __ldcg(a.part_ml + pt * COLS + c[u]);
           o[j][u] = __ldcg(reinterpret_cast<const float4*>(
-              a.part_o + pt * COLS * D + (ch[u] / 2 * COLS + c[u]) * 8 + (ch[u] & 1) * 4));
+              a.part_o + pt * COLS * D + cross_chunk<COLS, CHUNK>(ch[u], c[u])));
         }
       }
 #pragma unroll

@@ -160,21 +160,21 @@ __device__ __forceinline__ void regs_dec() {
 // spare.  One lane steps; a piece's fields are read again where they are used.
 struct WarpWalk {
   CrossWalk walk;
-  CrossPiece piece;
-  __device__ __forceinline__ bool next(const CrossArgs& a, bool with_keys) {
+  CrossPiece piece[2];  // (the softmax steps to the next piece while it is at one)
+  __device__ __forceinline__ bool next(const CrossArgs& a, bool with_keys, int to = 0) {
     bool ok = false;
     __syncwarp();
     if ((threadIdx.x & 31) == 0)
-      while ((ok = walk.next(a, kTiles * kCols, kKeys, kExtra, &piece)) && with_keys && piece.n == 0) {
+      while ((ok = walk.next(a, kTiles * kCols, kKeys, kExtra, &piece[to])) && with_keys && piece[to].n == 0) {
       }
     ok = __any_sync(0xffffffffu, ok);
     __syncwarp();
     return ok;
   }
-  __device__ __forceinline__ CrossPiece get() const {
+  __device__ __forceinline__ CrossPiece get(int from = 0) const {
     CrossPiece p;
     static_assert(sizeof(CrossPiece) % 4 == 0, "copied by words");
-    const volatile int* const src = reinterpret_cast<const volatile int*>(&piece);
+    const volatile int* const src = reinterpret_cast<const volatile int*>(&piece[from]);
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(CrossPiece) / 4); ++i) reinterpret_cast<int*>(&p)[i] = src[i];
     return p;
@@ -433,11 +433,20 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     // Scores in log2 units are s * mul: under a positive scale the maximum commutes
     // with the rounded product; another scale is applied to the scores one by one.
     const float mul = a.scale_log2 > 0.f ? a.scale_log2 : 1.f;
-    while (ok && walk.next(a, false)) {
+    // The piece at hand is walk.piece[at].  What a piece needs beside its tiles is done
+    // while the tensor cores have the scores in hand: its block ids are checked behind
+    // its first tile's weights, the walk goes on behind its second's.
+    int at = 1;
+    bool looked = false, more = false;
+    while (ok) {
+      if (!looked) more = walk.next(a, false, at ^ 1);
+      looked = false;
+      at ^= 1;
+      if (!more) break;
       int left, tiles;  // keys from this tile on, tiles to go
-      bool bad;
+      bool bad = false;
       {
-        const CrossPiece p = walk.get();
+        const CrossPiece p = walk.get(at);
         const bool mine = t < live_tiles(p);
         if (p.n == 0) {
           if (mine && t * kCols + col < p.live) {
@@ -453,12 +462,25 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
           step += tiles;
           continue;
         }
-        bad = __any_sync(0xffffffffu, cross_bad_block(a, p, kKeys, lane, 32));
       }
       float m_run = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool begun = false;
       for (; tiles > 0; --tiles, left -= kKeys, ++step, begun = true) {
+        // Rows past the end in the last block hold stale data, and 0 x NaN
+        // would poison O: tile A's warpgroup clears them before its first P V,
+        // while the scores are on their way
+        if (t == 0 && left < kKeys && left % kBlockSize) {
+          const int vi = 2 * step + 1;
+          if (!wait_all(FULL(vi % NS), (vi / NS) & 1)) { ok = false; break; }
+          unsigned char* const vt = sR + (vi % NS) * KT;
+          const int nr = kBlockSize - left % kBlockSize;
+          for (int i = col; i < nr * 8 * KB; i += kWg) {
+            const int h = i / (nr * 8), r = left + (i / 8) % nr;
+            *reinterpret_cast<uint4*>(vt + h * HALF + r * 128 + ((i % 8) << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
         if (aborted() || !wait_all(TB(t, SFULL), (sn++) & 1)) { ok = false; break; }
         tc::fence_after_sync();
         const bool plain = left >= kKeys && a.scale_log2 > 0.f;
@@ -530,19 +552,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
           if (!plain) prepare(s1, 1);
           weights(s1, mul, m_run, w, 16, lh);
         }
-        // Rows past the end in the last block hold stale data, and 0 x NaN
-        // would poison O: tile A's warpgroup clears them before its first P V
-        if (t == 0 && left < kKeys && left % kBlockSize) {
-          const int vi = 2 * step + 1;
-          if (!wait_all(FULL(vi % NS), (vi / NS) & 1)) { ok = false; break; }
-          unsigned char* const vt = sR + (vi % NS) * KT;
-          const int nr = kBlockSize - left % kBlockSize;
-          for (int i = col; i < nr * 8 * KB; i += kWg) {
-            const int h = i / (nr * 8), r = left + (i / 8) % nr;
-            *reinterpret_cast<uint4*>(vt + h * HALF + r * 128 + ((i % 8) << 4)) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        }
         store_p(s_addr, w);
         tc::fence_before_sync();
         mbar_arrive(TB(t, P0));
@@ -553,15 +562,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         mbar_arrive(TB(t, P0 + 1));
         l2[0] = __fadd2_rn(l2[0], lh[0]);
         l2[1] = __fadd2_rn(l2[1], lh[1]);
+        if (!begun) {
+          bad = __any_sync(0xffffffffu, cross_bad_block(a, walk.get(at), kKeys, lane, 32));
+        } else if (!looked) {
+          more = walk.next(a, false, at ^ 1);
+          looked = true;
+        }
       }
       if (!ok) break;
       // ---- the piece's O
-      const CrossPiece p = walk.get();
+      const CrossPiece p = walk.get(at);
       const float2 la = __fadd2_rn(l2[0], l2[1]);
       const float l_run = la.x + la.y;
       if (bad && lane == 0 && a.err_flag) atomicOr(a.err_flag, kErrBlockId);
-      if (!wait_all(TB(t, ODONE), (on++) & 1)) { ok = false; break; }
-      tc::fence_after_sync();
       const size_t pt = static_cast<size_t>(max(p.slot, 0)) * kTiles + t;
       // A piece of a cut item: if every other piece has stored its partial, this
       // one is merged with them straight from tensor memory, else it is stored
@@ -570,6 +583,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       bool store = false;
       float wgt = 1.f, L = l_run, M = m_run;  // this piece's weight, the item's sum and maximum
       bool zero = bad;
+      // Of the y-th other piece: its slot, m and l, dims from 32 q on.  Of two pieces the
+      // other's dims are read 32 ahead of their use, into v; its weight is wv.
+      int mine = 0;
+      float wv = 0.f;
+      auto slot_of = [&](int y) { return cross_tile<kTiles>(first, y + (y >= mine), t); };
+      auto ml_of = [&](int y) { return a.part_ml + slot_of(y) * kCols + col; };
+      auto dims_of = [&](int q, int y) {
+        return reinterpret_cast<const float4*>(a.part_o + slot_of(y) * kCols * D) + 8 * q * kCols + col;
+      };
       if (p.slot >= 0) {
         cross_chain(s_total, p, &first, &pieces);
         if (col == 0) s_total.old[t] = atomicAdd(a.count + 2 * first + t, 0u);
@@ -577,69 +599,30 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         store = s_total.old[t] != static_cast<unsigned>(pieces - 1);
         if (!store) {
           __threadfence();
-          for (int i = 0; i < pieces; ++i)
-            if (first + i != blockIdx.x) M = fmaxf(M, __ldcg(a.part_ml + cross_tile<kTiles>(first, i, t) * kCols + col).x);
+          mine = blockIdx.x - first;
+          const float2 ml0 = __ldcg(ml_of(0));
+          M = fmaxf(M, ml0.x);
+          for (int y = 1; y < pieces - 1; ++y) M = fmaxf(M, __ldcg(ml_of(y)).x);
           L = 0.f;
-          for (int i = 0; i < pieces; ++i) {
-            const float2 ml = first + i == blockIdx.x
-                                  ? make_float2(m_run, bad ? -1.f : l_run)
-                                  : __ldcg(a.part_ml + cross_tile<kTiles>(first, i, t) * kCols + col);
+          for (int x = 0; x < pieces; ++x) {
+            const float2 ml = x == mine ? make_float2(m_run, bad ? -1.f : l_run)
+                              : x == (mine == 0) ? ml0 : __ldcg(ml_of(x - (x > mine)));
             zero |= ml.y < 0.f;
             L = fmaf(cross_weight(ml.x, M), ml.y, L);
           }
+          wv = cross_weight(ml0.x, M);
           wgt = cross_weight(m_run, M);
           if (col == 0) a.count[2 * first + t] = 0;
         }
       }
+      if (!wait_all(TB(t, ODONE), (on++) & 1)) { ok = false; break; }
+      tc::fence_after_sync();
       const float inv = 1.f / L;
       const bool live = t * kCols + col < p.live;
       __nv_bfloat16* const dst = static_cast<__nv_bfloat16*>(a.out) +
                                  (p.base(a) + (live ? cross_column(a, t * kCols + col) : 0)) * D;
-      // (every lane runs the warp-wide TMEM loads; only live columns are stored)
-#pragma unroll 1
-      for (int q = 0; q < D / 32; ++q) {
-        uint32_t o[32];
-        tc::tmem_ld32(o_addr + 32 * q, o);
-        tc::tmem_wait_ld(o);
-        const int at = (4 * q * kCols + col) * 8;  // these dims in a partial
-        if (store) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(o[8 * i + e]);
-            cross_store8(a.part_o + pt * kCols * D + at + i * kCols * 8, v);
-          }
-          continue;
-        }
-        if (pieces > 1) {
-          float acc[32];
-#pragma unroll
-          for (int k = 0; k < 32; ++k) acc[k] = 0.f;
-          for (int x = 0; x < pieces; ++x) {
-            if (first + x == blockIdx.x) {
-#pragma unroll
-              for (int k = 0; k < 32; ++k) acc[k] = fmaf(wgt, __uint_as_float(o[k]), acc[k]);
-              continue;
-            }
-            const size_t xt = cross_tile<kTiles>(first, x, t);
-            const float wx = cross_weight(__ldcg(a.part_ml + xt * kCols + col).x, M);
-            float4 v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              v[i] = __ldcg(reinterpret_cast<const float4*>(a.part_o + xt * kCols * D + at + i / 2 * kCols * 8) + i % 2);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              acc[4 * i] = fmaf(wx, v[i].x, acc[4 * i]);
-              acc[4 * i + 1] = fmaf(wx, v[i].y, acc[4 * i + 1]);
-              acc[4 * i + 2] = fmaf(wx, v[i].z, acc[4 * i + 2]);
-              acc[4 * i + 3] = fmaf(wx, v[i].w, acc[4 * i + 3]);
-            }
-          }
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(acc[k]);
-        }
-        if (!live) continue;
+      auto emit = [&](int q, const uint32_t (&o)[32]) {  // dims 32 q to 32 q + 31 of the output
+        if (!live) return;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {  // 16 dims (32 bytes) at a time
           uint32_t v[8];
@@ -657,6 +640,75 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
             to[1] = make_uint4(v[4], v[5], v[6], v[7]);
           }
         }
+      };
+      // (every lane runs the warp-wide TMEM loads; only live columns are stored)
+      const bool pair = pieces == 2 && !store;
+      if (pair) {  // w_0 o_0 + w_1 o_1
+        float4 v[8];
+        const float4* const head = dims_of(0, 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __ldcg(head + i * kCols);
+#pragma unroll 1
+        for (int q = 0; q < D / 32; ++q) {
+          uint32_t o[32];
+          tc::tmem_ld32(o_addr + 32 * q, o);
+          tc::tmem_wait_ld(o);
+          const bool go_on = q + 1 < D / 32;
+          const float4* const src = dims_of(q + 1, 0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float own = __uint_as_float(o[4 * i + e]);
+              o[4 * i + e] = __float_as_uint(mine == 0 ? fmaf(wv, x[e], wgt * own) : fmaf(wgt, own, wv * x[e]));
+            }
+            if (go_on) v[i] = __ldcg(src + i * kCols);
+          }
+          emit(q, o);
+        }
+      }
+#pragma unroll 1
+      for (int q = 0; q < (pair ? 0 : D / 32); ++q) {
+        uint32_t o[32];
+        tc::tmem_ld32(o_addr + 32 * q, o);
+        tc::tmem_wait_ld(o);
+        const int pq = (8 * q * kCols + col) * 4;  // these dims in a partial
+        if (store) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<uint4*>(a.part_o + pt * kCols * D + pq + i * kCols * 4) =
+                make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          continue;
+        }
+        if (pieces > 1) {
+          float acc[32];
+          float4 v[8];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) acc[k] = 0.f;
+          for (int x = 0; x < pieces; ++x) {
+            if (x == mine) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k) acc[k] = fmaf(wgt, __uint_as_float(o[k]), acc[k]);
+              continue;
+            }
+            const int y = x - (x > mine);
+            const float wx = cross_weight(__ldcg(ml_of(y)).x, M);
+            const float4* const src = dims_of(q, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __ldcg(src + i * kCols);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              acc[4 * i] = fmaf(wx, v[i].x, acc[4 * i]);
+              acc[4 * i + 1] = fmaf(wx, v[i].y, acc[4 * i + 1]);
+              acc[4 * i + 2] = fmaf(wx, v[i].z, acc[4 * i + 2]);
+              acc[4 * i + 3] = fmaf(wx, v[i].w, acc[4 * i + 3]);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(acc[k]);
+        }
+        emit(q, o);
       }
       tc::fence_before_sync();  // (O has been read before this warpgroup's next P lets it be written)
       if (store) {
@@ -667,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         if (!group_sync()) { ok = false; break; }
         if (s_total.old[t] == static_cast<unsigned>(pieces - 1)) {
           __threadfence();
-          cross_merge<__nv_bfloat16, D, kCols, kTiles, 4, 2>(a, p, first, pieces, t, col, kWg);
+          cross_merge<__nv_bfloat16, D, kCols, kTiles, 4, 2, 4>(a, p, first, pieces, t, col, kWg);
         }
       }
     }
