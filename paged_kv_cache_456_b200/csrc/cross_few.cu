@@ -346,10 +346,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
         __threadfence();
         static_assert(kMergeFloats<COLS> <= kWarps * 8 * D, "the weights go where the exchange was");
         // (with more column groups the partials in flight would spill the tile loop's registers)
-        if (NT <= 2 && pieces <= kMergeSharedPieces && p.live * (D / 4) * 16 > kThreads)
+        if (NT <= 2 && pieces <= kMergeSharedPieces && p.live * (D / 4) * 16 > kThreads) {
           cross_merge_shared<__nv_bfloat16, D, COLS, 2, 8>(a, p, first, pieces, tid, kThreads, s_o);
-        else
+          __syncthreads();  // (the weights are read to its end: the next piece's states go there)
+        } else {
           cross_merge<__nv_bfloat16, D, COLS, 1, 1, 4>(a, p, first, pieces, 0, tid, kThreads);
+        }
       }
     }
   }

@@ -1,0 +1,57 @@
+"""pa_cross_attention where a CTA's share holds several pieces: what one piece leaves in shared memory, in the counters
+or in the workspace must not reach another.  Tolerances as in test_gpu_cross, whose 64-bit definition this uses."""
+import pytest
+import torch
+
+from paged_kv_cache_456_b200 import ops
+
+from tests.test_gpu_cross import Case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_456_b200 import build
+    build.build()
+    ops.library()
+
+
+def beside_a_load(c, repeats):
+    """The outputs of ``repeats`` calls while another stream keeps part of the SMs busy, so that CTAs start late and
+    unevenly."""
+    ws = c.workspace()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    outs = [torch.full_like(c.q, 7.0) for _ in range(repeats)]
+    x = torch.randn(1024, 1024, device="cuda")
+    y = torch.empty_like(x)
+    load = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        with torch.cuda.stream(load):
+            for n in range(1 + i % 3):
+                torch.matmul(x[:256 * (1 + (i + n) % 4)], x, out=y[:256 * (1 + (i + n) % 4)])
+        ops.cross_attention(out, c.q, c.k, c.v, c.tables, c.lens, c.qs, scale=c.scale, max_context_len=c.max_keys,
+                            workspace=ws, err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    return outs
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,long_rows,short_rows", [(2, 9, 3), (2, 5, 4), (1, 10, 8), (2, 1, 1), (4, 1, 3), (1, 1, 1)])
+@pytest.mark.parametrize("pairs,keys", [(20, 2000), (30, 9000), (4, 60000), (60, 1100)])
+def test_few_columns_a_merge_and_then_a_short_piece(D, G, long_rows, short_rows, pairs, keys):
+    """Items cut into 2 to 31 pieces, some of them of two columns, each followed by sequences of 1 to 128 keys, whose
+    pieces begin while slower warps may still be merging: up to 16 columns a (sequence, KV head) on average."""
+    rows, lens = [], []
+    for i in range(pairs):
+        rows += [long_rows, short_rows]
+        lens += [keys - 7 * i, (1, 16, 17, 100, 128)[i % 5]]
+    c = Case(tuple(rows), tuple(lens), hkv=2, G=G, D=D, behind=1)
+    outs = beside_a_load(c, 12)
+    c.check(outs[0])
+    for out in outs[1:]:
+        assert torch.equal(out.view(torch.int16), outs[0].view(torch.int16))
