@@ -119,7 +119,10 @@ struct CrossShare {
 struct CrossTotal {
   long long W;       // units of the call
   int workers;       // workers that have some
-  unsigned old[2];   // partials stored before this one, per column tile
+  // partials stored before this one, per column tile and parity of the piece's
+  // slot: a share has at most one cut piece of each, so that no word is written
+  // for a later piece while a slow warp still has to read it
+  unsigned old[2][2];
   long long scratch[16];  // (a long long per warp, two more; at most 14 warps)
 };
 

@@ -340,9 +340,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
       cross_chain(s_total, p, &first, &pieces);
       __threadfence();
       __syncthreads();
-      if (tid == 0) s_total.old[0] = atomicInc(a.count + first, pieces - 1);
+      if (tid == 0) s_total.old[0][0] = atomicInc(a.count + first, pieces - 1);
       __syncthreads();
-      if (s_total.old[0] == static_cast<unsigned>(pieces - 1)) {
+      if (s_total.old[0][0] == static_cast<unsigned>(pieces - 1)) {
         __threadfence();
         static_assert(kMergeFloats<COLS> <= kWarps * 8 * D, "the weights go where the exchange was");
         // (with more column groups the partials in flight would spill the tile loop's registers)

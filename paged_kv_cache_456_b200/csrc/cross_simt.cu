@@ -266,9 +266,9 @@ cross_simt_kernel(const __grid_constant__ CrossArgs a) {
       cross_chain(s_total, p, &first, &pieces);
       __threadfence();
       __syncthreads();
-      if (tid == 0) s_total.old[0] = atomicInc(a.count + first, pieces - 1);
+      if (tid == 0) s_total.old[0][0] = atomicInc(a.count + first, pieces - 1);
       __syncthreads();
-      if (s_total.old[0] == static_cast<unsigned>(pieces - 1)) {
+      if (s_total.old[0][0] == static_cast<unsigned>(pieces - 1)) {
         __threadfence();
         static_assert(kMergeFloats<kCols> <= 4 * kKeys * 2 * CPT, "the weights go where P was");
         if (pieces <= kMergeSharedPieces)

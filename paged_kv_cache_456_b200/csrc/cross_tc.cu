@@ -596,9 +596,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
       };
       if (p.slot >= 0) {
         cross_chain(s_total, p, &first, &pieces);
-        if (col == 0) s_total.old[t] = atomicAdd(a.count + 2 * first + t, 0u);
+        if (col == 0) s_total.old[t][p.slot & 1] = atomicAdd(a.count + 2 * first + t, 0u);
         if (!group_sync()) { ok = false; break; }
-        store = s_total.old[t] != static_cast<unsigned>(pieces - 1);
+        store = s_total.old[t][p.slot & 1] != static_cast<unsigned>(pieces - 1);
         if (!store) {
           __threadfence();
           mine = blockIdx.x - first;
@@ -717,9 +717,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         a.part_ml[pt * kCols + col] = make_float2(m_run, bad ? -1.f : l_run);
         __threadfence();
         if (!group_sync()) { ok = false; break; }
-        if (col == 0) s_total.old[t] = atomicInc(a.count + 2 * first + t, pieces - 1);
+        if (col == 0) s_total.old[t][p.slot & 1] = atomicInc(a.count + 2 * first + t, pieces - 1);
         if (!group_sync()) { ok = false; break; }
-        if (s_total.old[t] == static_cast<unsigned>(pieces - 1)) {
+        if (s_total.old[t][p.slot & 1] == static_cast<unsigned>(pieces - 1)) {
           __threadfence();
           cross_merge<__nv_bfloat16, D, kCols, kTiles, 4, 2, 4>(a, p, first, pieces, t, col, kWg);
         }

@@ -55,3 +55,16 @@ def test_few_columns_a_merge_and_then_a_short_piece(D, G, long_rows, short_rows,
     c.check(outs[0])
     for out in outs[1:]:
         assert torch.equal(out.view(torch.int16), outs[0].view(torch.int16))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,rows", [(1, 40), (4, 40), (8, 100)])
+@pytest.mark.parametrize("seqs,keys", [(90, 200), (100, 300), (37, 1000), (8, 5000), (200, 129)])
+def test_many_columns_a_cut_item_and_then_a_piece_of_one_tile(D, G, rows, seqs, keys):
+    """More than 32 columns: shares of one to a few tiles of 128 keys, so that a cut item's end is followed at once by
+    the first tile of the next cut item."""
+    c = Case(tuple(rows - i % 7 for i in range(seqs)), tuple(keys - i % 3 * 64 for i in range(seqs)), hkv=2, G=G, D=D)
+    outs = beside_a_load(c, 12)
+    c.check(outs[0])
+    for out in outs[1:]:
+        assert torch.equal(out.view(torch.int16), outs[0].view(torch.int16))
