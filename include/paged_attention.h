@@ -405,8 +405,11 @@ pa_status pa_prefill(void *out, const void *q, const void *k_cache, const void *
  *   workspace       pa_cross_attention_workspace_size() bytes, 16-byte
  *                   aligned, zero-filled once before its first use
  *                   (pa_decode_workspace_init); every call leaves it ready
- *                   for the next, of whatever sizes.  Two calls that may run
- *                   at the same time must not share one.
+ *                   for the next.  The size covers every call of the same
+ *                   heads, head_dim and dtype with at most num_query_tokens
+ *                   rows, of any number of sequences and any lengths; a
+ *                   larger workspace does for smaller calls.  Two calls that
+ *                   may run at the same time must not share one.
  *   Everything else, and the supported shapes, are as in pa_decode, but that
  *   num_q_heads <= 32768, num_query_tokens * num_q_heads < 2^31 and contexts
  *   are of at most 2^30 tokens (PA_ERR_UNSUPPORTED above).

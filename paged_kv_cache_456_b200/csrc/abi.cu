@@ -831,10 +831,8 @@ pa_status pa_cross_attention_workspace_size(int num_seqs, int num_query_tokens, 
   if (st != PA_OK) return st;
   DeviceInfo dev;
   if ((st = device_info(&dev)) != PA_OK) return st;
-  *bytes = pa::cross_layout(pa::cross_kernel(num_seqs, num_query_tokens, num_q_heads / num_kv_heads,
-                                             head_dim, elem_bytes(dtype)),
-                            head_dim, dev.sms)
-               .bytes;
+  *bytes = pa::cross_workspace_bytes(num_query_tokens, num_q_heads / num_kv_heads, head_dim,
+                                     elem_bytes(dtype), dev.sms);
   return PA_OK;
 }
 

@@ -6,6 +6,7 @@
 //   x_i = scale q[r][h] . K_i,   i = 0 .. n - 1.
 #include "cross_attention.h"
 
+#include <algorithm>
 #include <exception>
 #include <map>
 #include <mutex>
@@ -25,12 +26,21 @@ std::map<std::pair<int, const void*>, bool> g_ready;  // (device, kernel): its s
 
 }  // namespace
 
-CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes) {
-  const long long columns =
-      num_seqs > 0 ? (static_cast<long long>(num_rows) * group + num_seqs - 1) / num_seqs : 0;
+namespace {
+
+// the kernel for `columns` query columns a (sequence, KV head), on average
+CrossKernel kernel_of(long long columns, int head_dim, int elem_bytes) {
   if (elem_bytes == 4) return cross_simt_kernel_info(head_dim, columns);
   if (columns <= kFewColumns) return cross_few_kernel_info(head_dim, static_cast<int>(columns));
   return cross_tc_kernel_info(head_dim);
+}
+
+}  // namespace
+
+CrossKernel cross_kernel(int num_seqs, int num_rows, int group, int head_dim, int elem_bytes) {
+  const long long columns =
+      num_seqs > 0 ? (static_cast<long long>(num_rows) * group + num_seqs - 1) / num_seqs : 0;
+  return kernel_of(columns, head_dim, elem_bytes);
 }
 
 CrossLayout cross_layout(const CrossKernel& k, int head_dim, int num_sms) {
@@ -40,6 +50,18 @@ CrossLayout cross_layout(const CrossKernel& k, int head_dim, int num_sms) {
   l.o_off = up256(l.ml_off + slots * k.cols * sizeof(float2));
   l.bytes = up256(l.o_off + slots * k.cols * head_dim * sizeof(float));
   return l;
+}
+
+// Fewer sequences put more columns on each, up to all rows on one, and with
+// them another kernel and layout: the largest of those that up to `num_rows`
+// rows can reach.
+size_t cross_workspace_bytes(int num_rows, int group, int head_dim, int elem_bytes, int num_sms) {
+  constexpr long long kLastChoice = 65;  // (from here on the kernel is the same)
+  const long long most = std::min(static_cast<long long>(num_rows) * group, kLastChoice);
+  size_t bytes = 0;
+  for (long long columns = 0; columns <= most; ++columns)
+    bytes = std::max(bytes, cross_layout(kernel_of(columns, head_dim, elem_bytes), head_dim, num_sms).bytes);
+  return bytes;
 }
 
 cudaError_t launch_cross_attention(CrossArgs& a, const CrossKernel& k, int num_sms, cudaStream_t stream) {

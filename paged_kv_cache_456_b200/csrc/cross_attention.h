@@ -82,6 +82,8 @@ struct CrossLayout {
   size_t ml_off, o_off, bytes;
 };
 CrossLayout cross_layout(const CrossKernel& k, int head_dim, int num_sms);
+// what any call of at most `num_rows` rows needs, however many sequences share them
+size_t cross_workspace_bytes(int num_rows, int group, int head_dim, int elem_bytes, int num_sms);
 cudaError_t launch_cross_attention(CrossArgs& a, const CrossKernel& k, int num_sms, cudaStream_t stream);
 
 #ifdef __CUDACC__

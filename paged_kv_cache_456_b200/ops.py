@@ -336,7 +336,8 @@ def prefill(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 def make_cross_attention_workspace(num_seqs: int, num_query_tokens: int, num_q_heads: int,
                                    num_kv_heads: int, head_dim: int, max_context_len: int,
                                    dtype: torch.dtype = torch.bfloat16, device="cuda") -> torch.Tensor:
-    """A zero-filled workspace of the size ``pa_cross_attention`` needs."""
+    """A zero-filled workspace for ``pa_cross_attention`` calls of at most ``num_query_tokens`` rows, of
+    any number of sequences."""
     n = ctypes.c_size_t(0)
     with torch.cuda.device(device):
         _check(library().pa_cross_attention_workspace_size(

@@ -68,3 +68,19 @@ def test_many_columns_a_cut_item_and_then_a_piece_of_one_tile(D, G, rows, seqs, 
     c.check(outs[0])
     for out in outs[1:]:
         assert torch.equal(out.view(torch.int16), outs[0].view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G,rows", [(128, 4, 256), (64, 1, 64), (64, 8, 8), (128, 1, 33)])
+def test_a_workspace_for_the_largest_batch_does_for_what_is_left_of_it(dtype, D, G, rows):
+    """Sized once for many sequences, used as sequences leave and the same rows, or fewer, fall to fewer sequences."""
+    ws = ops.make_cross_attention_workspace(64, rows, 2 * G, 2, D, 500, dtype=torch.bfloat16 if dtype == "bf16"
+                                            else torch.float32)
+    for seqs in (64, 17, 8, 4, 2, 1):
+        for part in (1, 3):
+            share = [max(rows // part // seqs, 1)] * min(seqs, rows // part)
+            c = Case(tuple(share), tuple(500 - 5 * i for i in range(len(share))), dtype=dtype, hkv=2, G=G, D=D)
+            assert c.T <= rows
+            out, err = c.call(ws=ws)
+            assert err == 0
+            c.check(out)
