@@ -214,10 +214,11 @@ pa_status pa_reshape_and_cache(const void *key, const void *value, void *k_cache
  * and becomes
  *     theta = positions[axis][t] * inv_freq[i],   axis = pair_axis[i]
  *     (a, b) <- rot_scale * (a cos theta - b sin theta, a sin theta + b cos theta)
- * Dims from rotary_dim on are copied bit for bit.  theta is reduced in 64
- * bits, so far positions cost no accuracy (positions are taken as exact up
- * to 2^53); the products are fp32 and each result is rounded once
- * (nearest-even) to the element type.
+ * Dims from rotary_dim on are copied bit for bit.  theta is the exact
+ * product of position and fp32 frequency, reduced in more than 64 bits, so
+ * positions of up to 2^53 cost no accuracy (larger ones are first rounded to
+ * a double); its cosine and sine and the products are fp32, and each result is
+ * rounded once (nearest-even) to the element type.
  *
  *   q, q_out       [num_tokens] rows of num_q_heads * head_dim elements, row
  *                  t at t * q_stride (q_out_stride) elements.  q_out may be q

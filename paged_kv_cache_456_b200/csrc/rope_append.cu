@@ -11,9 +11,10 @@
 // an element.  What is not a stream is kept off it:
 //   * the angles.  A token's cos and sin are the same for all its heads, so a
 //     CTA computes them once into shared memory, rotary_dim / 2 per token.
-//     theta is formed and reduced in fp64 (positions of a million times
-//     frequencies near 1 leave fp32 with no fraction), as a fraction of a
-//     turn, which sincospif takes in fp32: |error| < 1e-7.
+//     theta is formed and reduced as a fraction of a turn in pairs of doubles (a
+//     plain fp64 product is off by theta 2^-53: 1e-4 at 2^40), and goes to fp32 in
+//     two parts, so that sine and cosine carry the error of sincospif (1 ulp)
+//     and one rounding, at positions of up to 2^53.
 //   * the slots: one division per token, not per element.
 // A thread's unit of work is two 16-byte chunks of one row: the two halves of
 // the same 8 (bf16) or 4 (fp32) pairs, or two chunks to copy.
@@ -54,6 +55,9 @@ union Chunk {
   T e[16 / sizeof(T)];
 };
 
+// 1 / (2 pi), rounded to double, and what that leaves
+constexpr double kTurnsPerRadian = 0.15915494309189535, kTurnsPerRadianLow = -9.839338337591243e-18;
+
 // rot_scale (cos, sin) of pair p of token t
 __device__ __forceinline__ float2 angle(const RopeArgs& a, int p, long long t) {
   int axis = 0;
@@ -64,10 +68,18 @@ __device__ __forceinline__ float2 angle(const RopeArgs& a, int p, long long t) {
       return make_float2(a.rot_scale, 0.f);
     }
   }
-  const double pos = static_cast<double>(a.positions[axis * a.num_tokens + t]);
-  const double turns = pos * static_cast<double>(a.inv_freq[p]) * 0.15915494309189533577;
-  float s, c;
-  sincospif(2.f * static_cast<float>(turns - rint(turns)), &s, &c);
+  // the product exactly (hi + lo), times 1 / (2 pi) in two doubles: turns + rest
+  const double pos = static_cast<double>(a.positions[axis * a.num_tokens + t]), freq = a.inv_freq[p];
+  const double hi = pos * freq, lo = fma(pos, freq, -hi);
+  const double turns = hi * kTurnsPerRadian;
+  const double rest = fma(hi, kTurnsPerRadianLow, fma(lo, kTurnsPerRadian, fma(hi, kTurnsPerRadian, -turns)));
+  double part = (turns - rint(turns)) + rest;
+  part = 2. * (part - rint(part));  // half turns, in [-1, 1]
+  // to fp32 in two parts: sine and cosine of the first, turned by the second (below 2^-25 half turns)
+  const float x = static_cast<float>(part), d = 3.14159265f * static_cast<float>(part - x);
+  float s0, c0;
+  sincospif(x, &s0, &c0);
+  const float s = fmaf(d, c0, s0), c = fmaf(-d, s0, c0);
   return make_float2(c * a.rot_scale, s * a.rot_scale);
 }
 
