@@ -34,7 +34,9 @@
 // (1.03 ms); an eighth to a half of the weights from a cubic on the FMA units
 // (0.94 to 0.99 ms).
 // A piece with at most 128 columns leaves tile B out.  Every mbarrier wait is
-// bounded; a wait that runs out sets PA_ERRBIT_TIMEOUT and every role leaves.
+// bounded, by what it waits for: one tile's work, or for the q warp and a
+// warpgroup whose column tile is left out the tiles of whole pieces.  A wait that
+// runs out sets PA_ERRBIT_TIMEOUT and every role leaves.
 #include <cstdint>
 #include <type_traits>
 
@@ -89,6 +91,20 @@ __device__ __forceinline__ bool wait_all(uint32_t bar, uint32_t parity) {
   if (!ok) {
     const uint64_t t0 = global_timer_ns();
     while (!(ok = try_wait(bar, parity)) && global_timer_ns() - t0 <= kWaitLimitNs) {
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+// The same for a wait through `tiles` tiles of other roles' work: that many
+// times the limit of one, given up as soon as another role gives up (which each
+// of them does within the limit of one tile).
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity, int tiles, const int* abort) {
+  bool ok = try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = global_timer_ns(), limit = kWaitLimitNs * static_cast<uint64_t>(tiles + 1);
+    while (!(ok = try_wait(bar, parity)) && *reinterpret_cast<const volatile int*>(abort) == 0 &&
+           global_timer_ns() - t0 <= limit) {
     }
   }
   return __all_sync(0xffffffffu, ok);
@@ -392,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     } else if (warp == kQWarp) {
       // ---------------- q rows: 128 / G rows x G heads a tile, by tensor loads (columns past
       // the sequence's last get other rows, or zeros past the tensor's end) -------------
-      int qn[kTiles] = {0, 0};
+      int qn[kTiles] = {0, 0}, before = 0;  // (the last piece's tiles)
       bool ok = true;
       const int rows = kCols >> a.group_log2;
       while (ok && walk.next(a, true)) {
@@ -400,7 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           if (t >= live_tiles(p) || !ok) continue;
-          if (aborted() || (qn[t] > 0 && !wait_all(TB(t, QEMPTY), (qn[t] - 1) & 1))) {
+          // (a wait through the last piece)
+          if (aborted() || (qn[t] > 0 && !wait_long(TB(t, QEMPTY), (qn[t] - 1) & 1, before, &s_abort))) {
             ok = false;
             continue;
           }
@@ -414,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
           }
           __syncwarp();
         }
+        before = p.t1 - p.t0;
       }
       if (!ok) timeout();
       for (int t = 0; t < kTiles; ++t)  // (the last loads land before the CTA can exit)
@@ -427,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
     const uint32_t s_addr = lane_base + t * kKeys, o_addr = lane_base + kTiles * kKeys + t * 128;
     const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     int step = 0, sn = 0, on = 0, syncs = 0;
+    int passed = 0;  // tiles of the pieces since this warpgroup's last one
     bool ok = true;
     auto group_sync = [&]() -> bool {  // the 128 threads of this warpgroup
       mbar_arrive(TB(t, SYNC));
@@ -462,9 +481,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_tc_kernel(const __grid_cons
         left = p.n - p.t0 * kKeys;
         if (!mine) {
           step += tiles;
+          passed += tiles;
           continue;
         }
       }
+      // (the first scores come when the pieces without this column tile are done)
+      if (passed > 0 && !wait_long(TB(t, SFULL), sn & 1, passed, &s_abort)) { ok = false; break; }
+      passed = 0;
       float m_run = -INFINITY;
       float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       bool begun = false;

@@ -84,3 +84,25 @@ def test_a_workspace_for_the_largest_batch_does_for_what_is_left_of_it(dtype, D,
             out, err = c.call(ws=ws)
             assert err == 0
             c.check(out)
+
+
+def repeated(rows, keys, heads, D, dtype, period=64):
+    """Sequences whose tables list ``period`` blocks over and over, one query head a KV head: a few cached tokens stand
+    for contexts of millions."""
+    c = Case(rows, (period * 16,) * len(rows), dtype=dtype, hkv=heads, G=1, D=D)
+    c.tables = c.tables[:, torch.arange(-(-max(keys) // 16), device="cuda") % period].contiguous()
+    c.lens.copy_(torch.tensor(keys, dtype=torch.int32))
+    c.max_keys = max(keys)
+    return c
+
+
+def test_a_column_tile_left_out_for_longer_than_one_wait_may_last():
+    """Eight sequences of 2^24 keys and 40 rows occupy every CTA for 1.4 s, in which the second column tile has nothing
+    to do; then come items of 200 rows.  (The limit of a wait for one tile's work is 1 s.)"""
+    period = 64
+    c = repeated((40,) * 8 + (200,), (1 << 24,) * 8 + (300,), 148, 64, "bf16", period)
+    out, err = c.call()
+    assert err == 0
+    assert torch.isfinite(out.float()).all()
+    c.keys = (period * 16,) * 8 + (300,)
+    c.check(out, skip=range(8))
