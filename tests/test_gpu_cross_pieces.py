@@ -106,3 +106,25 @@ def test_a_column_tile_left_out_for_longer_than_one_wait_may_last():
     assert torch.isfinite(out.float()).all()
     c.keys = (period * 16,) * 8 + (300,)
     c.check(out, skip=range(8))
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 1), ("bf16", 12), ("bf16", 40), ("f32", 1), ("f32", 40)])
+def test_a_million_keys_of_one_item_on_one_cta(dtype, rows):
+    """2^20 keys a KV head, as many KV heads as CTAs that hold them.  Beside the tolerance of the period's own sums (the
+    weights and their products repeat exactly), n keys are added up: fp32 n 2^-24 of A in the products and as much in
+    the weights; bf16 one truncation of at most 2^-23 for every 16 keys in the products, and sums of at least 16
+    weights rounded to nearest (2^-24) in the weights."""
+    n, period = 1 << 20, 64
+    c = repeated((rows,), (n,), 148, 64, dtype, period)
+    out, err = c.call()
+    assert err == 0
+    c.keys = (period * 16,)
+    want, tol = c.expected(0)
+    ids = c.tables[0, :period].long()
+    k, v = (x[ids].transpose(0, 1).reshape(148, -1, 64).double() for x in (c.k, c.v))
+    p = torch.softmax(c.scale * (c.q.double().transpose(0, 1) @ k.transpose(1, 2)), dim=-1)
+    a = (p @ v.abs()).transpose(0, 1)
+    sums = n * 2.0 ** -23 if dtype == "f32" else n / 16 * (2.0 ** -23 + 2.0 ** -24)
+    bound = tol + sums * a * (1 + torch.finfo(c.dt).eps / 2)
+    worst = ((out.double() - want).abs() / bound).max()
+    assert worst <= 1, f"worst error / tolerance {worst:.3f}"
