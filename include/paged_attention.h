@@ -397,7 +397,9 @@ pa_status pa_prefill(void *out, const void *q, const void *k_cache, const void *
  *                   from query_start[num_seqs] on are not touched.  A
  *                   sequence whose pair is out of order or out of range sets
  *                   PA_ERRBIT_QUERY; its rows may be left unwritten, and rows
- *                   that two pairs cover then hold either's result.
+ *                   that two pairs cover then hold either's result.  Where
+ *                   the pairs in order cover more than num_query_tokens rows
+ *                   can make work for, the bit is set and nothing written.
  *   context_lens    a length outside [0, min(max_context_len,
  *                   max_blocks_per_seq * 16)] sets PA_ERRBIT_CONTEXT_LEN, a
  *                   block id outside the cache among the blocks attended to

@@ -80,6 +80,8 @@ cudaError_t launch_cross_attention(CrossArgs& a, const CrossKernel& k, int num_s
   } catch (const std::exception&) {  // (the map's memory, the lock: nothing passes a C entry)
     return cudaErrorMemoryAllocation;
   }
+  const long long groups = ((static_cast<long long>(a.num_rows) << a.group_log2) / k.cols + a.num_seqs);
+  a.max_units = groups * a.num_kv_heads * (k.extra + (a.len_cap > 0 ? (a.len_cap + k.keys - 1) / k.keys : 1));
   void* params[] = {&a};
   return cudaLaunchKernel(k.fn, dim3(num_sms * k.ctas_per_sm), dim3(k.threads), params, k.smem, stream);
 }

@@ -49,6 +49,7 @@ struct CrossArgs {
   int group_log2;              // log2 of the query heads per KV head
   int max_blocks_per_seq, num_blocks, len_cap;
   float scale_log2;            // scale * log2(e)
+  long long max_units;         // of work that num_rows rows in order can make (set by the launcher)
   int32_t* err_flag;
   // workspace
   unsigned* count;             // [workers][column tiles]: partials stored of the item that begins
@@ -65,7 +66,7 @@ struct CrossKernel {
   const void* fn;              // __global__ void fn(CrossArgs)
   int threads, ctas_per_sm;
   size_t smem;                 // dynamic shared memory of a CTA
-  int cols, keys;              // columns of an item, keys of a tile
+  int cols, keys, extra;       // columns of an item, keys of a tile, units ahead of an item
   bool tma_q;                  // reads q through tm_q
 };
 // The kernel for a call (host-known sizes only).
@@ -152,17 +153,16 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
     for (int k = 0; k < MINE; ++k) {
       int bit = 0;
       mine[k] = s0 + k < s1 ? cross_seq(a, s0 + k, cols, &bit) : make_int4(0, 0, 0, 0);
-      local += units_of(mine[k]);
+      local += units_of(mine[k]);  // (at most 4 x 2^50)
       bits |= bit;
     }
   } else {
     for (int s = s0; s < s1; ++s) {
       int bit;
-      local += units_of(cross_seq(a, s, cols, &bit));
+      local = min(local + units_of(cross_seq(a, s, cols, &bit)), 1LL << 52);
       bits |= bit;
     }
   }
-  if (bits && blockIdx.x == 0 && a.err_flag) atomicOr(a.err_flag, bits);
   long long incl = local;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -182,6 +182,13 @@ __device__ __forceinline__ CrossShare cross_share(const CrossArgs& a, int cols, 
       W += scratch[i];
     }
   }
+  // Pairs of query_start that go back and forth can each be in order and cover the
+  // same rows many times over: such a call is refused, not worked through.
+  if (W > a.max_units) {
+    W = 0;
+    bits |= kErrQuery;
+  }
+  if (bits && blockIdx.x == 0 && a.err_flag) atomicOr(a.err_flag, bits);
   CrossShare x;
   const int w = blockIdx.x;
   const int workers = static_cast<int>(max(1LL, min(static_cast<long long>(gridDim.x), W)));

@@ -368,6 +368,7 @@ CrossKernel info() {
   k.smem = Shape<D>::SMEM;
   k.cols = 8 * NT;
   k.keys = kKeys;
+  k.extra = kExtra;
   return k;
 }
 

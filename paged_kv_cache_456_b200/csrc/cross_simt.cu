@@ -290,6 +290,7 @@ CrossKernel info() {
   k.smem = (static_cast<size_t>(8 * CPT) * D + 2 * kKeys * D + 4 * kKeys * 2 * CPT) * sizeof(float);
   k.cols = 8 * CPT;
   k.keys = kKeys;
+  k.extra = kExtra;
   return k;
 }
 

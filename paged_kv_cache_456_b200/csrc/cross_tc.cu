@@ -767,6 +767,7 @@ CrossKernel info() {
   k.smem = Shape<D>::SMEM;
   k.cols = kTiles * kCols;
   k.keys = kKeys;
+  k.extra = kExtra;
   k.tma_q = true;
   return k;
 }

@@ -128,3 +128,22 @@ def test_a_million_keys_of_one_item_on_one_cta(dtype, rows):
     bound = tol + sums * a * (1 + torch.finfo(c.dt).eps / 2)
     worst = ((out.double() - want).abs() / bound).max()
     assert worst <= 1, f"worst error / tolerance {worst:.3f}"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs,T", [(64, 300), (130, 300), (40, 9), (40, 900), (2000, 40)])
+def test_query_starts_that_go_back_and_forth_are_refused(dtype, seqs, T):
+    """0, T, 0, T, ...: every other pair is in order and covers all rows.  The call must not do their work over."""
+    c = Case((1,) * seqs, (100,) * seqs, dtype=dtype, hkv=1, G=4, D=64)
+    c.T = T
+    c.q = torch.randn(T, 4, 64, device="cuda").to(c.dt)
+    c.qs.copy_(torch.tensor([T * (s % 2) for s in range(seqs + 1)], dtype=torch.int32))
+    ws = c.workspace()
+    out, err = c.call(ws=ws)
+    assert err == ops.ERRBIT_QUERY
+    assert (out == 7.0).all()
+    # and the workspace is ready for a call that is in order
+    d = Case((T // 2, T - T // 2), (900, 70), dtype=dtype, hkv=1, G=4, D=64)
+    out, err = d.call(ws=ws)
+    assert err == 0
+    d.check(out)
