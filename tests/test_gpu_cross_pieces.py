@@ -147,3 +147,43 @@ def test_query_starts_that_go_back_and_forth_are_refused(dtype, seqs, T):
     out, err = d.call(ws=ws)
     assert err == 0
     d.check(out)
+
+
+def poisoned(ws):
+    """A workspace as it must be before its first use where it is read without having been written: the counters zero
+    (the first 16 KB), all else NaN."""
+    ws[16384:] = 255
+    return ws
+
+
+@pytest.mark.parametrize("dtype,rows", [("bf16", 2), ("bf16", 6), ("bf16", 28), ("f32", 2), ("f32", 28)])
+@pytest.mark.parametrize("seqs", [31, 33, 64, 127, 128, 129, 600])
+def test_numbers_of_sequences(dtype, rows, seqs):
+    """Up to 32 sequences every lane of a warp lays one out, up to 128 several, above the whole CTA: on each kernel (8,
+    24 and 112 columns a sequence at most), some sequences without rows and some without keys."""
+    g = torch.Generator().manual_seed(seqs + rows)
+    r = [int(x) for x in torch.randint(rows - rows // 4, rows + 1, (seqs,), generator=g)]
+    n = [int(x) for x in torch.randint(1, 260, (seqs,), generator=g)]
+    for i in range(0, seqs, 9):
+        r[i] = 0
+    for i in range(4, seqs, 11):
+        n[i] = 0
+    r[-1], n[-1], n[seqs // 2] = rows, 700, 3000
+    c = Case(tuple(r), tuple(n), dtype=dtype, hkv=2, G=4, D=64, before=1, behind=2)
+    ws = poisoned(c.workspace())
+    outs = [c.call(ws=ws) for _ in range(2)]
+    assert [err for _, err in outs] == [0, 0]
+    c.check(outs[0][0])
+    assert torch.equal(outs[0][0].view(torch.uint8), outs[1][0].view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D,G", [(64, 1), (64, 4), (128, 2), (128, 8)])
+@pytest.mark.parametrize("rows", [1, 3, 7, 12, 40, 150])
+@pytest.mark.parametrize("keys", [(40000,), (5000, 60, 2500)])
+def test_no_partial_is_read_that_was_not_stored(dtype, D, G, rows, keys):
+    """Cut items over a workspace that is NaN but for its counters."""
+    c = Case((rows,) * len(keys), keys, dtype=dtype, hkv=2, G=G, D=D)
+    out, err = c.call(ws=poisoned(c.workspace()))
+    assert err == 0
+    c.check(out)
