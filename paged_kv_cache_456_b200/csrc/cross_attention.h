@@ -376,14 +376,15 @@ __device__ __forceinline__ float cross_weight(float m, float M) { return m == -I
 
 // The merge of an item's column tile t (of TILES, COLS columns each) by
 // `team` threads, once all its partials are stored and visible.  A thread
-// takes 4 dims of a column at a time, UNITS of them and AHEAD pieces in flight.
-template <typename T, int D, int COLS, int TILES, int UNITS, int AHEAD, int CHUNK = 8>
+// takes 4 dims of a column at a time, UNITS of them and AHEAD pieces in flight;
+// with LANES, where 16 times as many threads as units are there, 16 lanes share one.
+template <typename T, int D, int COLS, int TILES, int UNITS, int AHEAD, int CHUNK = 8, bool LANES = false>
 __device__ __forceinline__ void cross_merge(const CrossArgs& a, const CrossPiece& p, int first, int pieces, int t,
                                             int i0, int team) {
   const int live = min(COLS, p.live - t * COLS);
   const int units = live * (D / 4);
-  if (pieces <= 16 && units * 16 <= team) {
-    // few units: 16 lanes of one, a piece each, summed by a fixed tree
+  if (LANES && pieces <= 16 && units * 16 <= team) {
+    // 16 lanes of a unit, a piece each, summed by a fixed tree
     const int u = i0 / 16, j = i0 % 16;
     const int x = min(u, units - 1), ch = x / (2 * live) * 2 + (x & 1), c = x % (2 * live) >> 1;
     float2 ml = make_float2(-INFINITY, 0.f);

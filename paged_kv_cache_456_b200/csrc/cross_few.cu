@@ -350,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_few_kernel(const __grid_con
           cross_merge_shared<__nv_bfloat16, D, COLS, 2, 8>(a, p, first, pieces, tid, kThreads, s_o);
           __syncthreads();  // (the weights are read to its end: the next piece's states go there)
         } else {
-          cross_merge<__nv_bfloat16, D, COLS, 1, 1, 4>(a, p, first, pieces, 0, tid, kThreads);
+          // (one column of 64 dims is 16 units)
+          cross_merge<__nv_bfloat16, D, COLS, 1, 1, 4, 8, D * 4 <= kThreads>(a, p, first, pieces, 0, tid, kThreads);
         }
       }
     }
