@@ -242,7 +242,8 @@ pa_status pa_reshape_and_cache(const void *key, const void *value, void *k_cache
  *                  stretched frequencies).
  * rotary_dim is a multiple of 16, at most head_dim; head_dim * element size,
  * every stride * element size and every buffer are multiples of 16 bytes;
- * any block_size >= 1.  Rows of different tokens must not overlap in q_out.
+ * any block_size >= 1; head_dim to 4096 and 65535 heads (PA_ERR_UNSUPPORTED
+ * above).  Rows of different tokens must not overlap, in any of the four.
  */
 typedef enum pa_rope_style {
     PA_ROPE_HALVES = 0,
@@ -386,7 +387,8 @@ pa_status pa_prefill(void *out, const void *q, const void *k_cache, const void *
  * Q = query_start[s+1] - query_start[s].  For every row r of sequence s and
  * query head h, with K_i, V_i of KV head h / (num_q_heads / num_kv_heads):
  *     out[r][h][:] = softmax_i(scale * q[r][h] . K_i) . V_i,  i = 0 .. n-1
- * n == 0 gives zero rows.  The states are written to the cache once, with
+ * n == 0 gives zero rows; a row whose scores are all -inf is NaN, as its
+ * softmax is.  The states are written to the cache once, with
  * pa_reshape_and_cache (or pa_rope_append), and read by every later step:
  * one row per sequence while generating, many rows for a prompt or an image.
  *

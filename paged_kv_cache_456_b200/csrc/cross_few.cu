@@ -4,8 +4,9 @@
 // An item is up to 8 NT query columns of one (sequence, KV head); a tile is one
 // block of 16 keys, which a warp takes whole:
 //   S^T[16 keys x 8]  = K q^T           mma.sync m16n8k16, fp32 accumulation
-//   P = 2^(S scale log2 e - m)          online per warp, bf16 for the product,
-//                                       summed in fp32 before that rounding
+//   P = 2^(S scale log2 e - m)          online per warp, bf16 for the product (as
+//                                       V is: an MMA takes one type), summed in
+//                                       fp32 before that rounding
 //   O^T[D x 8]       += V^T P
 // for each of the NT groups of 8 columns.  (With keys on the M side the work is
 // proportional to the columns there are; 128 query columns on the M side of a
@@ -39,6 +40,8 @@ struct Shape {
   static constexpr int SMEM = 1024 + kWarps * DEPTH * SLOT + kWarps * 8 * D * 4;
 };
 
+// 2^x, approximate, 0 below the smallest normal number: of a weight (at most 2^8) that
+// is rounded to bf16, and of a factor between two maxima
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

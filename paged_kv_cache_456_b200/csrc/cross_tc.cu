@@ -143,7 +143,12 @@ __device__ __forceinline__ void maxima(const uint32_t (&s)[32], float (&m)[4]) {
     for (int i = 0; i < 4; ++i) m[i] = max3(m[i], __uint_as_float(s[k + i]), __uint_as_float(s[k + i + 4]));
   }
 }
-// 2^(s mul - m) as bf16 pairs in w[at, at + 16), added up in l before the rounding
+// 2^(s mul - m) as bf16 pairs in w[at, at + 16), added up in l before the rounding.
+// (An MMA takes both operands in one type, and V is bf16.  Adding up the weights as
+// rounded instead would take two instructions more a pair, in the chain that this
+// kernel waits for, and gains little: the output's error falls by 1.5 % over 100
+// keys and 0.1 to 0.5 % over 1100 or 4096, computed in 64 bits for values of mean 0
+// to 2 deviations.)
 __device__ __forceinline__ void weights(const uint32_t (&s)[32], float mul, float m, uint32_t (&w)[32], int at,
                                         float2 (&l)[2]) {
   // (a column that saw only -inf: an offset of 0 keeps its weights at 0)

@@ -15,7 +15,8 @@
 //     plain fp64 product is off by theta 2^-53: 1e-4 at 2^40), and goes to fp32 in
 //     two parts, so that sine and cosine carry the error of sincospif (1 ulp)
 //     and one rounding, at positions of up to 2^53.
-//   * the slots: one division per token, not per element.
+//   * the slots: one division per token (and warp that works on it), not per
+//     element.
 // A thread's unit of work is two 16-byte chunks of one row: the two halves of
 // the same 8 (bf16) or 4 (fp32) pairs, or two chunks to copy.
 //
@@ -23,10 +24,10 @@
 // up to 512 bf16 or 256 fp32 elements, with any rotary_dim that leaves whole
 // units), a warp takes a token, or a slice of its rows: a lane keeps the same
 // place in every row, its angles in registers, and three or four rows in flight; no
-// division, no barrier.  Other shapes take a CTA per few tokens, its units laid
+// division a row, no barrier.  Other shapes take a CTA per few tokens, its units laid
 // end to end, angles read from shared memory per unit.  Measured on what both
-// can do, 16384 tokens of 48 rows of 256 bytes (402 MB): 67 us (91 %
-// of the copy rate) against 81; one token of as many rows: 2.7 against 2.4 us.
+// can do, 16384 tokens of 48 rows of 256 bytes (402 MB): 68.5 us (90 %
+// of the copy rate) against 81; one token of as many rows: 2.8 against 2.4 us.
 #include <algorithm>
 #include <cstdint>
 #include <type_traits>
