@@ -187,3 +187,54 @@ def test_no_partial_is_read_that_was_not_stored(dtype, D, G, rows, keys):
     out, err = c.call(ws=poisoned(c.workspace()))
     assert err == 0
     c.check(out)
+
+
+@pytest.mark.parametrize("first,second", [(("bf16", 1), ("bf16", 60)), (("bf16", 60), ("f32", 30)), (("f32", 1), ("bf16", 3)),
+                                          (("bf16", 60), ("bf16", 60))])
+def test_two_calls_at_once(first, second):
+    """On two streams, each with a workspace of its own."""
+    cases = [Case((rows,) * 5, (3000, 200, 17, 1111, 640), dtype=dtype, G=2, D=64, seed=i)
+             for i, (dtype, rows) in enumerate((first, second))]
+    alone = [c.call()[0] for c in cases]
+    streams, spaces = [torch.cuda.Stream() for _ in cases], [c.workspace() for c in cases]
+    outs = [[torch.full_like(c.q, 7.0) for _ in range(10)] for c in cases]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for c, s, ws, out in zip(cases, streams, spaces, outs):
+            ops.cross_attention(out[i], c.q, c.k, c.v, c.tables, c.lens, c.qs, scale=c.scale, max_context_len=c.max_keys,
+                                workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for c, want, out in zip(cases, alone, outs):
+        c.check(want)
+        for o in out:
+            assert torch.equal(o.view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [(1, 2), (9, 4)])
+def test_thousands_of_heads(dtype, D, rows):
+    c = Case(rows, (40, 21), dtype=dtype, hkv=2050, G=8, D=D, behind=1)
+    out, err = c.call()
+    assert err == 0
+    c.check(out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 12, 90])
+@pytest.mark.parametrize("at", [0, 700, 2499])
+def test_one_bad_block_poisons_every_piece_of_its_sequence(dtype, rows, at):
+    """A bad id in the first, a middle or the last piece of cut items: the sequence's rows are zeros, the others' right."""
+    c = Case((rows, rows, 3), (300, 40000, 129), dtype=dtype, hkv=2, G=2, D=64)
+    ws = poisoned(c.workspace())
+    good = int(c.tables[1, at])
+    for bad in (c.k.shape[0], -1, good):
+        c.tables[1, at] = bad
+        out, err = c.call(ws=ws)
+        if bad == good:
+            assert err == 0
+            c.check(out)
+        else:
+            assert err == ops.ERRBIT_BLOCK_ID
+            assert (out[c.starts[1]:c.starts[2]] == 0).all()
+            c.check(out, skip=(1,))

@@ -53,3 +53,18 @@ def test_cosine_and_sine_at_any_distance(D, rot, adjacent, far):
     for got, ref in ((cos, want[..., 0]), (sin, want[..., 1])):
         err, bound = (got - ref).abs(), (2.0 ** -23 + 2.0 ** -24) * ref.abs() + 2.0 ** -45
         assert (err <= bound).all(), f"worst error / bound {(err / bound).max():.3f}, error {err.max():.2e}"
+
+
+def test_the_farthest_positions_there_are():
+    """Past 2^53 a position counts as the double nearest to it: the angle is that double's."""
+    far = [(1 << 63) - 1, -(1 << 63), (1 << 53) + 1, (1 << 60) + 12345, -(1 << 62) - 1]
+    freq = [1.0, 0.5, 0.001, 3.0e-5, 2.0 ** -40, 0.0, 7.0, 1.0e-20]
+    pos = torch.tensor(far)
+    x = torch.zeros(len(far), 1, 16)
+    x[..., :8] = 1.0
+    out = ops.rope_append(torch.empty(len(far), 1, 16, device="cuda"), x.cuda(), None, None, None, None, None, pos.cuda(),
+                          torch.tensor(freq, device="cuda")).cpu().double()[:, 0]
+    want = torch.tensor([[exact(float(p), f) for f in torch.tensor(freq).tolist()] for p in far], dtype=torch.float64)
+    # two doubles hold a fraction of a turn of 2^63 radians to about 2^63 2^-104
+    for got, ref in ((out[:, :8], want[..., 0]), (out[:, 8:], want[..., 1])):
+        assert ((got - ref).abs() <= (2.0 ** -23 + 2.0 ** -24) * ref.abs() + 2.0 ** -39).all()
